@@ -22,6 +22,9 @@ KDA_DTYPE_F32, KDA_DTYPE_BF16 = 0, 1
 KDA_FLAG_L2NORM_QK = 1
 KDA_FLAG_OUT_NORM_GATE = 2
 KDA_FLAG_RAW_GATE = 4
+KDA_FLAG_SILU = 8
+KDA_FLAG_SOFTPLUS = 16
+KDA_FLAG_PER_TOKEN = 32
 
 # Every symbol include/kda.h declares.
 EXPORTED_SYMBOLS = ("kda_chunk_fwd", "kda_recurrent_step", "kda_status_string",
@@ -33,7 +36,13 @@ EXPORTED_SYMBOLS = ("kda_chunk_fwd", "kda_recurrent_step", "kda_status_string",
                     "kda_chunk_bwd_workspace_bytes", "kda_set_prefill_segments",
                     "kda_prefill_segments", "kda_chunk_transition",
                     "kda_chunk_transition_workspace_bytes", "kda_state_affine",
-                    "kda_set_prefill_dual")
+                    "kda_set_prefill_dual",
+                    "kda_short_conv_fwd", "kda_short_conv_step", "kda_short_conv_bwd",
+                    "kda_short_conv_bwd_workspace_bytes", "kda_ssm_scan_fwd", "kda_ssm_step",
+                    "kda_ssm_scan_bwd", "kda_ssm_scan_fwd_workspace_bytes",
+                    "kda_ssm_scan_bwd_workspace_bytes", "kda_group_norm_fwd",
+                    "kda_group_norm_bwd", "kda_group_norm_fwd_workspace_bytes",
+                    "kda_group_norm_bwd_workspace_bytes")
 
 _lib = None
 
@@ -113,6 +122,28 @@ def load_library(path: Optional[str] = None):
     lib.kda_chunk_transition_workspace_bytes.restype = sz
     lib.kda_state_affine.argtypes = [fp, fp, fp, fp, ci, ci, ci, ci, vp]
     lib.kda_state_affine.restype = ci
+    cu = ctypes.c_uint
+    calls = {
+        "kda_short_conv_fwd": [vp] * 7 + [ci] * 6 + [cu, vp],
+        "kda_short_conv_step": [vp] * 5 + [ci] * 4 + [cu, vp],
+        "kda_short_conv_bwd": [vp] * 11 + [ci] * 6 + [cu, vp, sz, vp],
+        "kda_ssm_scan_fwd": [vp] * 12 + [ci] * 7 + [cu, vp, sz, vp],
+        "kda_ssm_step": [vp] * 10 + [ci] * 5 + [cu, vp],
+        "kda_ssm_scan_bwd": [vp] * 21 + [ci] * 7 + [cu, vp, sz, vp],
+        "kda_group_norm_fwd": [vp] * 4 + [cf] + [vp] * 3 + [ci] * 6 + [cu, vp, sz, vp],
+        "kda_group_norm_bwd": [vp] * 10 + [ci] * 6 + [cu, vp, sz, vp],
+    }
+    sizes = {
+        "kda_short_conv_bwd_workspace_bytes": [ci] * 7,
+        "kda_ssm_scan_fwd_workspace_bytes": [ci] * 8,
+        "kda_ssm_scan_bwd_workspace_bytes": [ci] * 8,
+        "kda_group_norm_fwd_workspace_bytes": [ci] * 7 + [cu],
+        "kda_group_norm_bwd_workspace_bytes": [ci] * 7 + [cu],
+    }
+    for names, restype in ((calls, ci), (sizes, sz)):
+        for name, argtypes in names.items():
+            getattr(lib, name).argtypes = argtypes
+            getattr(lib, name).restype = restype
     _lib = lib
     return lib
 

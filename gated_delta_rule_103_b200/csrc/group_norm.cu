@@ -1,0 +1,779 @@
+// Group norm with an optional SiLU, channels last:
+//
+//     xhat = (x - mean) rstd,   v = xhat w + b,   y = v or silu(v)
+//
+// with mean and 1 / sqrt(var + eps) over a sample's tokens and the C / G
+// channels of a group.  A sample is a token (the per-head norm of a mixer's
+// output) or a whole sequence.
+//
+// Per token, a row of one group is contiguous and fits the registers of a few
+// lanes: one read, one write (memory-bound).  Over sequences, three launches:
+// partial statistics of units of tokens, their combination in a fixed order,
+// and the normalisation (x is read twice; what fits the 126 MB L2 comes from
+// HBM once).
+//
+// Statistics are held as (count, mean, sum of squared deviations) and merged
+// pairwise by
+//     m = m1 + (m2 - m1) n2 / n,   q = q1 + q2 + (m2 - m1)^2 n1 n2 / n
+// so that a mean far from zero costs no digits; within a thread the sums run
+// over x - k with k the thread's first value.
+#include "layer.h"
+#include "layer_common.cuh"
+
+namespace kda {
+namespace {
+
+using namespace layer;
+
+struct Moments {
+    float n, m, q;
+    __device__ __forceinline__ void merge(const Moments& o)
+    {
+        const float t = n + o.n;
+        if (t <= 0.f) return;
+        const float d = o.m - m, r = o.n / t;
+        m = fmaf(d, r, m);
+        q += o.q + d * d * n * r;
+        n = t;
+    }
+};
+
+template <int LANES>
+__device__ __forceinline__ float lane_sum(float v)
+{
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// ---- per token --------------------------------------------------------------
+// LANES lanes hold one row of Cg = C / G values, NV vectors of V each (lane l:
+// values (l + i LANES) V).  A lane keeps to one group, so that its weights
+// stay in registers while it walks the tokens.
+template <typename T, int V, int LANES, int NV, bool kBwd>
+__global__ void __launch_bounds__(256)
+kda_norm_rows_kernel(const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
+                     T* __restrict__ out, float* __restrict__ mean, float* __restrict__ rstd,
+                     const T* __restrict__ d_out, float* __restrict__ grad_x, float* __restrict__ part,
+                     long long rows, int G, int Cg, int walkers, float eps, int act)
+{
+    // walker k of group g takes rows k, k + walkers, ...
+    const long long id = ((long long)blockIdx.x * 256 + threadIdx.x) / LANES;
+    const int lane = threadIdx.x & (LANES - 1);
+    const int g = (int)(id % G);
+    const long long k = id / G;
+    const bool live = k < walkers;  // a whole row's lanes agree; the warp stays together for the sums
+    float w[NV][V], b[NV][V], dw[NV][V], db[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (lane + i * LANES) * V;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            w[i][j] = c < Cg && weight ? weight[(size_t)g * Cg + c + j] : 1.f;
+            b[i][j] = c < Cg && bias ? bias[(size_t)g * Cg + c + j] : 0.f;
+            dw[i][j] = db[i][j] = 0.f;
+        }
+    }
+    const float inv = 1.f / (float)Cg;
+    const long long steps = (rows + walkers - 1) / walkers;
+    for (long long s = 0; s < steps; ++s) {
+        const long long r = k + s * walkers;
+        const bool here = live && r < rows;
+        const size_t at = ((size_t)(here ? r : 0) * G + g) * Cg;
+        float v[NV][V];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (lane + i * LANES) * V;
+            if (here && c < Cg) load_vec<V>(x + at + c, v[i]);
+            else
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[i][j] = 0.f;
+        }
+        if constexpr (!kBwd) {
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) sum += v[i][j];
+            const float m = lane_sum<LANES>(sum) * inv;
+            float sq = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (lane + i * LANES) * V;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float d = c < Cg ? v[i][j] - m : 0.f;
+                    sq = fmaf(d, d, sq);
+                }
+            }
+            const float rs = 1.f / sqrtf(fmaf(lane_sum<LANES>(sq), inv, eps));
+            if (!here) continue;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (lane + i * LANES) * V;
+                if (c >= Cg) continue;
+                float y[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    y[j] = fmaf((v[i][j] - m) * rs, w[i][j], b[i][j]);
+                    if (act) y[j] = silu(y[j]);
+                }
+                store_vec<V>(out + at + c, y);
+            }
+            if (lane == 0) {
+                mean[(size_t)r * G + g] = m;
+                rstd[(size_t)r * G + g] = rs;
+            }
+        } else {
+            const float m = here ? mean[(size_t)r * G + g] : 0.f, rs = here ? rstd[(size_t)r * G + g] : 0.f;
+            float dy[NV][V], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (lane + i * LANES) * V;
+                if (here && c < Cg) load_vec<V>(d_out + at + c, dy[i]);
+                else
+#pragma unroll
+                    for (int j = 0; j < V; ++j) dy[i][j] = 0.f;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    v[i][j] = (v[i][j] - m) * rs;  // xhat
+                    if (act) dy[i][j] *= silu_slope(fmaf(v[i][j], w[i][j], b[i][j]));
+                    if (!here || c >= Cg) v[i][j] = dy[i][j] = 0.f;
+                    dw[i][j] = fmaf(dy[i][j], v[i][j], dw[i][j]);
+                    db[i][j] += dy[i][j];
+                    dy[i][j] *= w[i][j];
+                    s1 += dy[i][j];
+                    s2 = fmaf(dy[i][j], v[i][j], s2);
+                }
+            }
+            s1 = lane_sum<LANES>(s1) * inv;
+            s2 = lane_sum<LANES>(s2) * inv;
+            if (!here) continue;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (lane + i * LANES) * V;
+                if (c >= Cg) continue;
+                float dx[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) dx[j] = rs * (dy[i][j] - s1 - v[i][j] * s2);
+                store_vec<V>(grad_x + at + c, dx);
+            }
+        }
+    }
+    if (kBwd && live) {
+        const size_t C = (size_t)G * Cg;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (lane + i * LANES) * V;
+            if (c >= Cg) continue;
+            store_vec<V>(part + ((size_t)k * 2) * C + (size_t)g * Cg + c, dw[i]);
+            store_vec<V>(part + ((size_t)k * 2 + 1) * C + (size_t)g * Cg + c, db[i]);
+        }
+    }
+}
+
+__device__ __forceinline__ float block_sum(float v, float* red)
+{
+    v = lane_sum<32>(v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += red[i];
+    return s;
+}
+
+// Rows too long for a warp's registers: a block per (walker, group), the row
+// read again from L1/L2 for each pass.  The parameters' sums stay in the
+// block's own rows of `part`, where only this thread adds to them.
+template <typename T, int V, bool kBwd>
+__global__ void __launch_bounds__(256)
+kda_norm_long_rows_kernel(const T* __restrict__ x, const float* __restrict__ weight,
+                          const float* __restrict__ bias, T* __restrict__ out, float* __restrict__ mean,
+                          float* __restrict__ rstd, const T* __restrict__ d_out, float* __restrict__ grad_x,
+                          float* __restrict__ part, long long rows, int G, int Cg, int walkers, float eps, int act)
+{
+    __shared__ float red[8];
+    const int g = blockIdx.x % G, k = blockIdx.x / G;
+    const float inv = 1.f / (float)Cg;
+    const size_t C = (size_t)G * Cg;
+    const float* w = weight ? weight + (size_t)g * Cg : nullptr;
+    const float* b = bias ? bias + (size_t)g * Cg : nullptr;
+    float* pw = part + ((size_t)k * 2) * C + (size_t)g * Cg;
+    float* pb = pw + C;
+    if (kBwd)
+        for (int c = threadIdx.x * V; c < Cg; c += 256 * V)
+#pragma unroll
+            for (int j = 0; j < V; ++j) pw[c + j] = pb[c + j] = 0.f;
+    for (long long r = k; r < rows; r += walkers) {
+        const size_t at = ((size_t)r * G + g) * Cg;
+        if constexpr (!kBwd) {
+            float sum = 0.f, sq = 0.f, v[V];
+            for (int c = threadIdx.x * V; c < Cg; c += 256 * V) {
+                load_vec<V>(x + at + c, v);
+#pragma unroll
+                for (int j = 0; j < V; ++j) sum += v[j];
+            }
+            const float m = block_sum(sum, red) * inv;
+            for (int c = threadIdx.x * V; c < Cg; c += 256 * V) {
+                load_vec<V>(x + at + c, v);
+#pragma unroll
+                for (int j = 0; j < V; ++j) sq = fmaf(v[j] - m, v[j] - m, sq);
+            }
+            const float rs = 1.f / sqrtf(fmaf(block_sum(sq, red), inv, eps));
+            for (int c = threadIdx.x * V; c < Cg; c += 256 * V) {
+                load_vec<V>(x + at + c, v);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    v[j] = fmaf((v[j] - m) * rs, w ? w[c + j] : 1.f, b ? b[c + j] : 0.f);
+                    if (act) v[j] = silu(v[j]);
+                }
+                store_vec<V>(out + at + c, v);
+            }
+            if (threadIdx.x == 0) {
+                mean[(size_t)r * G + g] = m;
+                rstd[(size_t)r * G + g] = rs;
+            }
+        } else {
+            const float m = mean[(size_t)r * G + g], rs = rstd[(size_t)r * G + g];
+            float s1 = 0.f, s2 = 0.f, v[V], dy[V];
+            for (int c = threadIdx.x * V; c < Cg; c += 256 * V) {
+                load_vec<V>(x + at + c, v);
+                load_vec<V>(d_out + at + c, dy);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float xh = (v[j] - m) * rs, wj = w ? w[c + j] : 1.f;
+                    if (act) dy[j] *= silu_slope(fmaf(xh, wj, b ? b[c + j] : 0.f));
+                    pw[c + j] = fmaf(dy[j], xh, pw[c + j]);
+                    pb[c + j] += dy[j];
+                    s1 = fmaf(dy[j], wj, s1);
+                    s2 = fmaf(dy[j] * wj, xh, s2);
+                }
+            }
+            s1 = block_sum(s1, red) * inv;
+            s2 = block_sum(s2, red) * inv;
+            for (int c = threadIdx.x * V; c < Cg; c += 256 * V) {
+                load_vec<V>(x + at + c, v);
+                load_vec<V>(d_out + at + c, dy);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float xh = (v[j] - m) * rs, wj = w ? w[c + j] : 1.f;
+                    if (act) dy[j] *= silu_slope(fmaf(xh, wj, b ? b[c + j] : 0.f));
+                    dy[j] = rs * (dy[j] * wj - s1 - xh * s2);
+                }
+                store_vec<V>(grad_x + at + c, dy);
+            }
+        }
+    }
+}
+
+// ---- over sequences ---------------------------------------------------------
+// A block takes one unit of tokens and `gb` whole groups.  Where gb groups fit
+// its 256 threads (cols = gb Cg / V columns), a thread keeps to one column and
+// strides over the tokens; a group wider than 256 columns has a block of its
+// own whose threads walk the columns too.
+struct Layout {
+    int cols, cpg, gb, ngb, ty;  // columns per block and per group, groups per block, blocks across, token lanes
+};
+
+template <int V>
+Layout layout_of(int C, int G)
+{
+    Layout l;
+    l.cpg = C / G / V;
+    if (l.cpg >= 256) {
+        l.gb = 1;
+        l.cols = l.cpg;
+        l.ty = 1;
+    } else {
+        l.gb = 256 / l.cpg < G ? 256 / l.cpg : G;
+        l.cols = l.gb * l.cpg;
+        l.ty = 256 / l.cols;
+    }
+    l.ngb = (G + l.gb - 1) / l.gb;
+    return l;
+}
+
+// Partial statistics: part[(unit G + g) 2 ..] = mean and squared deviations of
+// the unit's tokens of group g (its count is known from the unit).
+template <typename T, int V>
+__global__ void __launch_bounds__(256)
+kda_norm_stats_kernel(const T* __restrict__ x, float* __restrict__ part, Units units, Layout l, int C, int G)
+{
+    __shared__ float sn[256], sm[256], sq[256];
+    int n, seg;
+    long long a, b;
+    const long long unit = blockIdx.x / l.ngb;
+    if (!units.locate(unit, n, seg, a, b)) return;
+    const int g0 = (int)(blockIdx.x % l.ngb) * l.gb;
+    const int groups = G - g0 < l.gb ? G - g0 : l.gb;
+    const int wide = l.cols > 256;
+    const int ty = wide ? 0 : threadIdx.x / l.cols;
+    const int cx = wide ? threadIdx.x : threadIdx.x % l.cols;
+    Moments mo = {0.f, 0.f, 0.f};
+    if (ty < l.ty && cx < groups * l.cpg) {
+        for (int c = cx; c < groups * l.cpg; c += wide ? 256 : l.cols) {
+            const T* p = x + (size_t)g0 * l.cpg * V + (size_t)c * V;
+            float k = 0.f, s1 = 0.f, s2 = 0.f;
+            long long cnt = 0;
+            for (long long t = a + ty; t < b; t += l.ty) {
+                float v[V];
+                load_vec<V>(p + (size_t)t * C, v);
+                if (cnt == 0) k = v[0];
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float d = v[j] - k;
+                    s1 += d;
+                    s2 = fmaf(d, d, s2);
+                }
+                cnt += V;
+            }
+            if (cnt > 0) {
+                const float f = (float)cnt, d = s1 / f;
+                const Moments o = {f, k + d, fmaxf(s2 - s1 * d, 0.f)};
+                mo.merge(o);
+            }
+        }
+    }
+    sn[threadIdx.x] = mo.n;
+    sm[threadIdx.x] = mo.m;
+    sq[threadIdx.x] = mo.q;
+    __syncthreads();
+    // a warp per group: its threads' moments lane by lane, then across lanes
+    const int lane = threadIdx.x & 31;
+    for (int g = threadIdx.x >> 5; g < groups; g += 8) {
+        const int per = wide ? 256 : l.cpg * l.ty;
+        Moments t = {0.f, 0.f, 0.f};
+        for (int i = lane; i < per; i += 32) {
+            const int src = wide ? i : (i / l.cpg) * l.cols + g * l.cpg + i % l.cpg;
+            const Moments o = {sn[src], sm[src], sq[src]};
+            t.merge(o);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const Moments u = {__shfl_xor_sync(0xffffffffu, t.n, o), __shfl_xor_sync(0xffffffffu, t.m, o),
+                               __shfl_xor_sync(0xffffffffu, t.q, o)};
+            t.merge(u);
+        }
+        if (lane == 0) {
+            part[((size_t)unit * G + g0 + g) * 2] = t.m;
+            part[((size_t)unit * G + g0 + g) * 2 + 1] = t.q;
+        }
+    }
+}
+
+// mean and rstd of every (sequence, group): a warp merges its units.
+__global__ void __launch_bounds__(256)
+kda_norm_merge_kernel(const float* __restrict__ part, float* __restrict__ mean, float* __restrict__ rstd,
+                      Units units, int G, int Cg, float eps)
+{
+    const long long id = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (id >= (long long)units.s.N * G) return;
+    const int n = (int)(id / G), g = (int)(id % G);
+    long long a, b;
+    units.s.bounds(n, a, b);
+    const long long first = units.first(n);
+    const int cnt = units.count(n);
+    Moments t = {0.f, 0.f, 0.f};
+    for (int i = lane; i < cnt; i += 32) {
+        const long long left = b - a - (long long)i * units.len;
+        const float2 p = *reinterpret_cast<const float2*>(part + ((size_t)(first + i) * G + g) * 2);
+        const Moments o = {(float)(left < units.len ? left : units.len) * (float)Cg, p.x, p.y};
+        t.merge(o);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const Moments u = {__shfl_xor_sync(0xffffffffu, t.n, o), __shfl_xor_sync(0xffffffffu, t.m, o),
+                           __shfl_xor_sync(0xffffffffu, t.q, o)};
+        t.merge(u);
+    }
+    if (lane == 0) {
+        mean[id] = t.m;  // 0 of an empty sequence
+        rstd[id] = 1.f / sqrtf((t.n > 0.f ? t.q / t.n : 0.f) + eps);
+    }
+}
+
+// The normalisation (forward), or dx from the sums of the kernels below
+// (backward; sums[(n G + g) 2 ..] = mean of k and of k xhat).
+template <typename T, int V, bool kBwd>
+__global__ void __launch_bounds__(256)
+kda_norm_apply_kernel(const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
+                      T* __restrict__ out, const float* __restrict__ mean, const float* __restrict__ rstd,
+                      const T* __restrict__ d_out, const float* __restrict__ sums, float* __restrict__ grad_x,
+                      Units units, Layout l, int C, int G, int act)
+{
+    int n, seg;
+    long long a, b;
+    if (!units.locate(blockIdx.x / l.ngb, n, seg, a, b)) return;
+    const int g0 = (int)(blockIdx.x % l.ngb) * l.gb;
+    const int groups = G - g0 < l.gb ? G - g0 : l.gb;
+    const int wide = l.cols > 256;
+    const int ty = wide ? 0 : threadIdx.x / l.cols;
+    const int cx = wide ? threadIdx.x : threadIdx.x % l.cols;
+    if (ty >= l.ty) return;
+    for (int c = cx; c < groups * l.cpg; c += wide ? 256 : l.cols) {
+        const int ch = (g0 * l.cpg + c) * V;
+        const size_t ng = (size_t)n * G + g0 + c / l.cpg;
+        const float m = mean[ng], rs = rstd[ng];
+        float w[V], bb[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            w[j] = weight ? weight[ch + j] : 1.f;
+            bb[j] = bias ? bias[ch + j] : 0.f;
+        }
+        const float k1 = kBwd ? sums[ng * 2] : 0.f, k2 = kBwd ? sums[ng * 2 + 1] : 0.f;
+#pragma unroll 4
+        for (long long t = a + ty; t < b; t += l.ty) {
+            const size_t at = (size_t)t * C + ch;
+            float v[V];
+            load_vec<V>(x + at, v);
+            if constexpr (!kBwd) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    v[j] = fmaf((v[j] - m) * rs, w[j], bb[j]);
+                    if (act) v[j] = silu(v[j]);
+                }
+                store_vec<V>(out + at, v);
+            } else {
+                float dy[V];
+                load_vec<V>(d_out + at, dy);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float xh = (v[j] - m) * rs;
+                    if (act) dy[j] *= silu_slope(fmaf(xh, w[j], bb[j]));
+                    dy[j] = rs * (dy[j] * w[j] - k1 - xh * k2);
+                }
+                store_vec<V>(grad_x + at, dy);
+            }
+        }
+    }
+}
+
+// Backward sums of a unit: part[unit][0][c] = sum dv xhat, part[unit][1][c] = sum dv.
+template <typename T, int V>
+__global__ void __launch_bounds__(256)
+kda_norm_bwd_sums_kernel(const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
+                         const float* __restrict__ mean, const float* __restrict__ rstd,
+                         const T* __restrict__ d_out, float* __restrict__ part, Units units, Layout l, int C, int G,
+                         int act)
+{
+    __shared__ float red[2 * V * 256];
+    int n, seg;
+    long long a, b;
+    const long long unit = blockIdx.x / l.ngb;
+    if (!units.locate(unit, n, seg, a, b)) return;
+    const int g0 = (int)(blockIdx.x % l.ngb) * l.gb;
+    const int groups = G - g0 < l.gb ? G - g0 : l.gb;
+    const int wide = l.cols > 256;
+    const int ty = wide ? 0 : threadIdx.x / l.cols;
+    const int cx = wide ? threadIdx.x : threadIdx.x % l.cols;
+    for (int c = cx; c < groups * l.cpg; c += wide ? 256 : l.cols) {
+        if (ty >= l.ty) break;
+        const int ch = (g0 * l.cpg + c) * V;
+        const size_t ng = (size_t)n * G + g0 + c / l.cpg;
+        const float m = mean[ng], rs = rstd[ng];
+        float w[V], bb[V], dw[V], db[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            w[j] = weight ? weight[ch + j] : 1.f;
+            bb[j] = bias ? bias[ch + j] : 0.f;
+            dw[j] = db[j] = 0.f;
+        }
+#pragma unroll 4
+        for (long long t = a + ty; t < b; t += l.ty) {
+            const size_t at = (size_t)t * C + ch;
+            float v[V], dy[V];
+            load_vec<V>(x + at, v);
+            load_vec<V>(d_out + at, dy);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float xh = (v[j] - m) * rs;
+                if (act) dy[j] *= silu_slope(fmaf(xh, w[j], bb[j]));
+                dw[j] = fmaf(dy[j], xh, dw[j]);
+                db[j] += dy[j];
+            }
+        }
+        if (wide) {
+            store_vec<V>(part + ((size_t)unit * 2) * C + ch, dw);
+            store_vec<V>(part + ((size_t)unit * 2 + 1) * C + ch, db);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                red[j * 256 + threadIdx.x] = dw[j];
+                red[(V + j) * 256 + threadIdx.x] = db[j];
+            }
+        }
+    }
+    if (wide) return;  // the whole block agrees
+    __syncthreads();
+    for (int q = threadIdx.x; q < 2 * groups * l.cpg * V; q += 256) {
+        const int which = q / (groups * l.cpg * V), c = q - which * groups * l.cpg * V;
+        float s = 0.f;
+        for (int y = 0; y < l.ty; ++y) s += red[(which * V + c % V) * 256 + y * l.cols + c / V];
+        part[((size_t)unit * 2 + which) * C + g0 * l.cpg * V + c] = s;
+    }
+}
+
+// From the units' sums: of every (sequence, group) the means of k = dv w and
+// k xhat, a warp each ...
+__global__ void __launch_bounds__(256)
+kda_norm_bwd_merge_kernel(const float* __restrict__ part, const float* __restrict__ weight,
+                          float* __restrict__ sums, Units units, int C, int G)
+{
+    const long long id = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (id >= (long long)units.s.N * G) return;
+    const int n = (int)(id / G), g = (int)(id % G), Cg = C / G;
+    long long a, b;
+    units.s.bounds(n, a, b);
+    const long long first = units.first(n);
+    const int cnt = units.count(n);
+    float s1 = 0.f, s2 = 0.f;
+    for (long long i = lane; i < (long long)cnt * Cg; i += 32) {
+        const long long unit = first + i / Cg;
+        const int c = g * Cg + (int)(i % Cg);
+        const float w = weight ? weight[c] : 1.f;
+        s2 = fmaf(w, part[((size_t)unit * 2) * C + c], s2);
+        s1 = fmaf(w, part[((size_t)unit * 2 + 1) * C + c], s1);
+    }
+    s1 = lane_sum<32>(s1);
+    s2 = lane_sum<32>(s2);
+    if (lane == 0) {
+        const float inv = b > a ? 1.f / ((float)(b - a) * (float)Cg) : 0.f;
+        sums[id * 2] = s1 * inv;
+        sums[id * 2 + 1] = s2 * inv;
+    }
+}
+
+// ... and the parameters' gradients: 32 channels per block, eight lanes over
+// the parts.  Slots that no unit fills are passed over.
+__global__ void __launch_bounds__(256)
+kda_norm_params_kernel(const float* __restrict__ part, float* __restrict__ grad_weight,
+                       float* __restrict__ grad_bias, Units units, int by_unit, long long parts, int C)
+{
+    __shared__ float red[2][8][33];
+    const int lane = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    float sw = 0.f, sb = 0.f;
+    for (long long i = y; i < parts; i += 8) {
+        if (by_unit) {
+            int n, seg;
+            long long a, b;
+            if (!units.locate(i, n, seg, a, b)) continue;
+        }
+        if (c < C) {
+            sw += part[((size_t)i * 2) * C + c];
+            sb += part[((size_t)i * 2 + 1) * C + c];
+        }
+    }
+    red[0][y][lane] = sw;
+    red[1][y][lane] = sb;
+    __syncthreads();
+    if (y < 2 && c < C) {
+        float t = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t += red[y][k][lane];
+        if (y == 0 && grad_weight) grad_weight[c] = t;
+        if (y == 1 && grad_bias) grad_bias[c] = t;
+    }
+}
+
+// ---- host -------------------------------------------------------------------
+
+constexpr int kUnitTokens = 64;
+
+Units units_of(const int32_t* cu, int packed, int B, int T, int N)
+{
+    Units u;
+    u.s.cu = cu;
+    u.s.N = N;
+    u.s.T = T;
+    u.s.total = (long long)B * T;
+    u.len = kUnitTokens;
+    u.per_seq = T > 0 ? (T + u.len - 1) / u.len : 1;
+    (void)packed;
+    return u;
+}
+long long slots_of(int B, int T, int N, int packed)
+{
+    return packed ? ((long long)B * T) / kUnitTokens + N
+                  : (long long)N * (T > 0 ? (T + kUnitTokens - 1) / kUnitTokens : 1);
+}
+
+// vector width: the widest of 8 (bf16 only), 4, 2 and 1 that divides a group
+int width_of(int Cg, kda_dtype dtype)
+{
+    if (dtype == KDA_DTYPE_BF16 && Cg % 8 == 0) return 8;
+    return Cg % 4 == 0 ? 4 : (Cg % 2 == 0 ? 2 : 1);
+}
+
+// Lanes per row and vectors per lane of the per-token kernel; lanes = 0: rows
+// too long for it.
+struct RowShape {
+    int V, lanes, nv, walkers;
+    long long blocks;
+};
+RowShape row_shape(long long rows, int C, int G, kda_dtype dtype, bool bwd)
+{
+    RowShape r = {};
+    const int Cg = C / G;
+    r.V = width_of(Cg, dtype);
+    const int vecs = Cg / r.V;
+    r.lanes = 1;
+    while (r.lanes < 32 && r.lanes < vecs) r.lanes <<= 1;
+    r.nv = 1;
+    while (r.nv * r.lanes < vecs) r.nv <<= 1;
+    const int per_block = r.nv <= 4 ? 256 / r.lanes : 1;  // rows in flight
+    if (r.nv > 4) r.lanes = r.nv = 0;
+    // enough walkers for every SM's warps, none without a row
+    const long long want = (long long)sm_count() * (bwd ? 4 : 8) * per_block;
+    long long w = (want + G - 1) / G;
+    if (w > rows) w = rows;
+    if (w < 1) w = 1;
+    r.walkers = (int)w;
+    r.blocks = (w * G + per_block - 1) / per_block;
+    return r;
+}
+
+template <typename T, int V, int LANES, bool kBwd>
+cudaError_t rows_nv(const NormArgs& a, const RowShape& r, cudaStream_t st)
+{
+    const long long rows = (long long)a.B * a.T;
+#define KDA_NORM_ROWS(NV)                                                                                      \
+    kda_norm_rows_kernel<T, V, LANES, NV, kBwd><<<(unsigned)r.blocks, 256, 0, st>>>(                           \
+        (const T*)a.x, a.weight, a.bias, (T*)a.out, a.mean, a.rstd, (const T*)a.d_out, a.grad_x,               \
+        (float*)a.workspace, rows, a.G, a.C / a.G, r.walkers, a.eps, a.silu)
+    if constexpr (LANES < 32) {
+        KDA_NORM_ROWS(1);
+    } else {
+        if (r.nv == 1) KDA_NORM_ROWS(1);
+        else if (r.nv == 2) KDA_NORM_ROWS(2);
+        else KDA_NORM_ROWS(4);
+    }
+#undef KDA_NORM_ROWS
+    return cudaGetLastError();
+}
+
+template <typename T, int V, bool kBwd>
+cudaError_t rows(const NormArgs& a, const RowShape& r, cudaStream_t st)
+{
+    switch (r.lanes) {
+        case 1: return rows_nv<T, V, 1, kBwd>(a, r, st);
+        case 2: return rows_nv<T, V, 2, kBwd>(a, r, st);
+        case 4: return rows_nv<T, V, 4, kBwd>(a, r, st);
+        case 8: return rows_nv<T, V, 8, kBwd>(a, r, st);
+        case 16: return rows_nv<T, V, 16, kBwd>(a, r, st);
+        case 32: return rows_nv<T, V, 32, kBwd>(a, r, st);
+    }
+    kda_norm_long_rows_kernel<T, V, kBwd><<<(unsigned)r.blocks, 256, 0, st>>>(
+        (const T*)a.x, a.weight, a.bias, (T*)a.out, a.mean, a.rstd, (const T*)a.d_out, a.grad_x,
+        (float*)a.workspace, (long long)a.B * a.T, a.G, a.C / a.G, r.walkers, a.eps, a.silu);
+    return cudaGetLastError();
+}
+
+template <typename T, int V>
+cudaError_t forward(const NormArgs& a, kda_dtype dtype, cudaStream_t st)
+{
+    if (a.per_token) {
+        if ((long long)a.B * a.T == 0) return cudaSuccess;
+        return rows<T, V, false>(a, row_shape((long long)a.B * a.T, a.C, a.G, dtype, false), st);
+    }
+    const Units u = units_of(a.cu_seqlens, a.cu_seqlens != nullptr, a.B, a.T, a.N);
+    const Layout l = layout_of<V>(a.C, a.G);
+    const long long blocks = u.slots() * l.ngb;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    float* part = (float*)a.workspace;
+    if (blocks > 0) {
+        kda_norm_stats_kernel<T, V><<<(unsigned)blocks, 256, 0, st>>>((const T*)a.x, part, u, l, a.C, a.G);
+        if (cudaError_t e = cudaGetLastError()) return e;
+    }
+    const long long ng = (long long)a.N * a.G;
+    kda_norm_merge_kernel<<<(unsigned)((ng + 7) / 8), 256, 0, st>>>(part, a.mean, a.rstd, u, a.G, a.C / a.G, a.eps);
+    if (cudaError_t e = cudaGetLastError()) return e;
+    if (blocks > 0)
+        kda_norm_apply_kernel<T, V, false><<<(unsigned)blocks, 256, 0, st>>>(
+            (const T*)a.x, a.weight, a.bias, (T*)a.out, a.mean, a.rstd, nullptr, nullptr, nullptr, u, l, a.C, a.G,
+            a.silu);
+    return cudaGetLastError();
+}
+
+template <typename T, int V>
+cudaError_t backward(const NormArgs& a, kda_dtype dtype, cudaStream_t st)
+{
+    const long long tokens = (long long)a.B * a.T;
+    const unsigned pblocks = (unsigned)((a.C + 31) / 32);
+    float* part = (float*)a.workspace;
+    Units u = units_of(a.cu_seqlens, a.cu_seqlens != nullptr, a.B, a.T, a.N);
+    if (a.per_token) {
+        const RowShape r = row_shape(tokens, a.C, a.G, dtype, true);
+        if (tokens > 0)
+            if (cudaError_t e = rows<T, V, true>(a, r, st)) return e;
+        kda_norm_params_kernel<<<pblocks, 256, 0, st>>>(part, a.grad_weight, a.grad_bias, u, 0,
+                                                        tokens > 0 ? r.walkers : 0, a.C);
+        return cudaGetLastError();
+    }
+    const Layout l = layout_of<V>(a.C, a.G);
+    const long long slots = u.slots(), blocks = slots * l.ngb;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    float* sums = part + (size_t)slots * 2 * a.C;
+    if (blocks > 0) {
+        kda_norm_bwd_sums_kernel<T, V><<<(unsigned)blocks, 256, 0, st>>>(
+            (const T*)a.x, a.weight, a.bias, a.mean, a.rstd, (const T*)a.d_out, part, u, l, a.C, a.G, a.silu);
+        if (cudaError_t e = cudaGetLastError()) return e;
+    }
+    const long long ng = (long long)a.N * a.G;
+    if (ng > 0) {
+        kda_norm_bwd_merge_kernel<<<(unsigned)((ng + 7) / 8), 256, 0, st>>>(part, a.weight, sums, u, a.C, a.G);
+        if (cudaError_t e = cudaGetLastError()) return e;
+    }
+    kda_norm_params_kernel<<<pblocks, 256, 0, st>>>(part, a.grad_weight, a.grad_bias, u, 1, slots, a.C);
+    if (cudaError_t e = cudaGetLastError()) return e;
+    if (blocks > 0)
+        kda_norm_apply_kernel<T, V, true><<<(unsigned)blocks, 256, 0, st>>>(
+            (const T*)a.x, a.weight, a.bias, nullptr, a.mean, a.rstd, (const T*)a.d_out, sums, a.grad_x, u, l, a.C,
+            a.G, a.silu);
+    return cudaGetLastError();
+}
+
+template <typename T, int V>
+cudaError_t run(const NormArgs& a, kda_dtype dtype, bool bwd, cudaStream_t st)
+{
+    return bwd ? backward<T, V>(a, dtype, st) : forward<T, V>(a, dtype, st);
+}
+
+cudaError_t dispatch(const NormArgs& a, kda_dtype dtype, bool bwd, cudaStream_t st)
+{
+    const int V = width_of(a.C / a.G, dtype);
+    if (dtype == KDA_DTYPE_F32) {
+        if (V == 4) return run<float, 4>(a, dtype, bwd, st);
+        if (V == 2) return run<float, 2>(a, dtype, bwd, st);
+        return run<float, 1>(a, dtype, bwd, st);
+    }
+    if (V == 8) return run<__nv_bfloat16, 8>(a, dtype, bwd, st);
+    if (V == 4) return run<__nv_bfloat16, 4>(a, dtype, bwd, st);
+    if (V == 2) return run<__nv_bfloat16, 2>(a, dtype, bwd, st);
+    return run<__nv_bfloat16, 1>(a, dtype, bwd, st);
+}
+
+}  // namespace
+
+size_t norm_fwd_workspace(int B, int T, int, int G, int N, int per_token, int packed, kda_dtype)
+{
+    if (per_token) return 0;
+    return (size_t)slots_of(B, T, N, packed) * G * 2 * sizeof(float);
+}
+
+size_t norm_bwd_workspace(int B, int T, int C, int G, int N, int per_token, int packed, kda_dtype dtype)
+{
+    if (per_token) {
+        if ((long long)B * T == 0) return 0;
+        return (size_t)row_shape((long long)B * T, C, G, dtype, true).walkers * 2 * C * sizeof(float);
+    }
+    return (size_t)slots_of(B, T, N, packed) * 2 * C * sizeof(float) + (size_t)N * G * 2 * sizeof(float);
+}
+
+cudaError_t launch_norm_fwd(const NormArgs& a, kda_dtype dtype, cudaStream_t st) { return dispatch(a, dtype, false, st); }
+cudaError_t launch_norm_bwd(const NormArgs& a, kda_dtype dtype, cudaStream_t st) { return dispatch(a, dtype, true, st); }
+
+}  // namespace kda

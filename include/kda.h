@@ -77,7 +77,15 @@ enum {
      * one taken): `log_alpha` holds the gate's pre-activations z (fp32, any
      * finite value) and the kernels use log alpha = log sigmoid(z) =
      * -softplus(-z).  The per-chunk precondition applies to log sigmoid(z). */
-    KDA_FLAG_RAW_GATE = 4
+    KDA_FLAG_RAW_GATE = 4,
+    /* kda_short_conv_*, kda_group_norm_*: the result goes through
+     * silu(v) = v / (1 + e^-v). */
+    KDA_FLAG_SILU = 8,
+    /* kda_ssm_*: the step is softplus(delta + delta_bias), not their sum. */
+    KDA_FLAG_SOFTPLUS = 16,
+    /* kda_group_norm_*: statistics of every token on its own, not of whole
+     * sequences. */
+    KDA_FLAG_PER_TOKEN = 32
 };
 
 /*
@@ -351,6 +359,173 @@ kda_status kda_chunk_bwd(const void* q, const void* k, const void* v,
  * cu_seqlens.  0 for sizes the call would reject.
  */
 size_t kda_chunk_bwd_workspace_bytes(int B, int T, int H, int N, int packed, kda_dtype dtype);
+
+/* ---------------------------------------------------------------------------
+ * Layer operators around the recurrences.  A recurrent mixer's layer is a
+ * short causal convolution in front ("深度解读报告" 3.2: ShortConv and Swish on
+ * the paths to q, k and v), the recurrence (KDA, or the diagonal state-space
+ * scan below) and a norm of its output ("深度解读报告" 3.2: head-wise).
+ *
+ * Conventions as above, and:
+ *  - dtype is the type of every per-token tensor; parameters, scan states,
+ *    statistics and all gradients are fp32.  Any channel count is taken.
+ *  - cu_seqlens [N + 1] int32 on the device, or NULL, as for kda_chunk_fwd:
+ *    with it B must be 1, without it N must equal B.  Rows of a packed call
+ *    that belong to no sequence are neither read nor written (per token,
+ *    kda_group_norm_* takes every row and does not read cu_seqlens).
+ *    Sequences may be empty.
+ *  - B * T up to 2^31 - 1, channels up to 2^24; more: KDA_ERR_UNSUPPORTED.
+ *  - No output may overlap another tensor of the call, except that
+ *    final_state may be the same pointer as initial_state.
+ *  - Results do not depend on what else runs: sums are taken in a fixed order.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * kda_short_conv_fwd -- causal depthwise convolution over the last W tokens:
+ *
+ *     v[t, c] = bias[c] + sum_{j < W} weight[c, j] x[t - W + 1 + j, c]
+ *     out     = v, or silu(v) with KDA_FLAG_SILU
+ *
+ *   x, out         [B, T, C]      dtype
+ *   weight         [C, W]         fp32, W = 2, 3 or 4 (others: KDA_ERR_UNSUPPORTED)
+ *   bias           [C]            fp32 or NULL (zero)
+ *   initial_state  [N, W - 1, C]  dtype or NULL (zero): the rows before each
+ *                  sequence's first token, oldest first
+ *   final_state    [N, W - 1, C]  dtype or NULL: the last W - 1 rows of
+ *                  (initial_state ++ x), for the next call
+ */
+kda_status kda_short_conv_fwd(const void* x, const float* weight, const float* bias,
+                              const void* initial_state, const int32_t* cu_seqlens,
+                              void* out, void* final_state,
+                              int B, int T, int C, int W, int N,
+                              kda_dtype dtype, unsigned flags, cudaStream_t stream);
+
+/*
+ * kda_short_conv_step -- one token for each of N sequences (x, out [N, C]);
+ * state [N, W - 1, C] dtype is used and shifted by one row in place.
+ */
+kda_status kda_short_conv_step(const void* x, const float* weight, const float* bias,
+                               void* state, void* out, int N, int C, int W,
+                               kda_dtype dtype, unsigned flags, cudaStream_t stream);
+
+/*
+ * kda_short_conv_bwd -- backward pass of kda_short_conv_fwd, from its inputs
+ * and the adjoints d_out [B, T, C] (dtype) and d_final_state [N, W - 1, C]
+ * (fp32, or NULL: zero).  Writes fp32 grad_x [B, T, C], grad_weight [C, W],
+ * grad_bias [C] (or NULL) and grad_initial_state [N, W - 1, C] (or NULL).
+ * workspace: kda_short_conv_bwd_workspace_bytes(), rules as for kda_chunk_bwd.
+ */
+kda_status kda_short_conv_bwd(const void* x, const float* weight, const float* bias,
+                              const void* initial_state, const int32_t* cu_seqlens,
+                              const void* d_out, const float* d_final_state,
+                              float* grad_x, float* grad_weight, float* grad_bias,
+                              float* grad_initial_state,
+                              int B, int T, int C, int W, int N, kda_dtype dtype, unsigned flags,
+                              void* workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t kda_short_conv_bwd_workspace_bytes(int B, int T, int C, int W, int N, int packed,
+                                          kda_dtype dtype);
+
+/*
+ * kda_ssm_scan_fwd -- selective state-space scan: a diagonal recurrence per
+ * channel with S states, its step, input and output vectors from the token.
+ * For channel d of group g = d / (D / G):
+ *
+ *     dt        = delta + delta_bias, or its softplus with KDA_FLAG_SOFTPLUS
+ *     h[d, s]   = exp(dt A[d, s]) h[d, s] + dt u B[g, s]
+ *     y         = sum_s h[d, s] C[g, s] + skip[d] u
+ *     out       = y, or y silu(z) where z is given
+ *
+ *   u, delta, out  [B, T, D]     dtype
+ *   A              [D, S]        fp32 (negative for a decaying state)
+ *   Bm, Cm         [B, T, G, S]  dtype; G divides D, S up to 128
+ *   skip, delta_bias  [D]        fp32 or NULL (zero)
+ *   z              [B, T, D]     dtype or NULL
+ *   initial_state, final_state   [N, D, S] fp32 or NULL, as for kda_chunk_fwd
+ * States and sums are fp32.  workspace: kda_ssm_scan_fwd_workspace_bytes()
+ * (0 where the channels alone fill the GPU), rules as for kda_chunk_fwd;
+ * `packed` is nonzero when the call passes cu_seqlens.
+ */
+kda_status kda_ssm_scan_fwd(const void* u, const void* delta, const float* A, const void* Bm,
+                            const void* Cm, const float* skip, const void* z,
+                            const float* delta_bias, const float* initial_state,
+                            const int32_t* cu_seqlens, void* out, float* final_state,
+                            int B, int T, int D, int S, int G, int N,
+                            kda_dtype dtype, unsigned flags,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t kda_ssm_scan_fwd_workspace_bytes(int B, int T, int D, int S, int G, int N, int packed,
+                                        kda_dtype dtype);
+
+/*
+ * kda_ssm_step -- one token for each of N sequences: u, delta, z, out [N, D],
+ * Bm, Cm [N, G, S]; state [N, D, S] fp32 is read and written once in place.
+ */
+kda_status kda_ssm_step(const void* u, const void* delta, const float* A, const void* Bm,
+                        const void* Cm, const float* skip, const void* z,
+                        const float* delta_bias, float* state, void* out,
+                        int N, int D, int S, int G, kda_dtype dtype, unsigned flags,
+                        cudaStream_t stream);
+
+/*
+ * kda_ssm_scan_bwd -- backward pass of kda_ssm_scan_fwd, from its inputs and
+ * the adjoints d_out [B, T, D] (dtype) and d_final_state [N, D, S] (fp32, or
+ * NULL: zero).  Writes, all fp32: grad_u, grad_delta [B, T, D], grad_A [D, S],
+ * grad_B, grad_C [B, T, G, S], grad_z [B, T, D] (read and written only where z
+ * is given), and, each unless NULL, grad_skip, grad_delta_bias [D] and
+ * grad_initial_state [N, D, S].  workspace: kda_ssm_scan_bwd_workspace_bytes()
+ * (the state every 8 or 16 tokens and the sums over channels and tokens),
+ * rules as for kda_chunk_bwd.
+ */
+kda_status kda_ssm_scan_bwd(const void* u, const void* delta, const float* A, const void* Bm,
+                            const void* Cm, const float* skip, const void* z,
+                            const float* delta_bias, const float* initial_state,
+                            const int32_t* cu_seqlens, const void* d_out,
+                            const float* d_final_state, float* grad_u, float* grad_delta,
+                            float* grad_A, float* grad_B, float* grad_C, float* grad_skip,
+                            float* grad_z, float* grad_delta_bias, float* grad_initial_state,
+                            int B, int T, int D, int S, int G, int N,
+                            kda_dtype dtype, unsigned flags,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t kda_ssm_scan_bwd_workspace_bytes(int B, int T, int D, int S, int G, int N, int packed,
+                                        kda_dtype dtype);
+
+/*
+ * kda_group_norm_fwd -- group norm, channels last: the C channels in G groups
+ * of C / G (G divides C),
+ *
+ *     out = (x - mean) rstd weight + bias, through silu with KDA_FLAG_SILU
+ *
+ * with mean and rstd = 1 / sqrt(var + eps) (var the mean squared deviation)
+ * over a group's channels and the tokens of a sample: a whole sequence, or
+ * with KDA_FLAG_PER_TOKEN each token (the norm of a mixer's heads).
+ *
+ *   x, out       [B, T, C]  dtype
+ *   weight, bias [C]        fp32 or NULL (one, zero)
+ *   mean, rstd   [samples, G] fp32, written: N samples, or B * T per token.
+ *                An empty sequence has mean 0 and rstd 1 / sqrt(eps).
+ *   eps          > 0
+ * workspace: kda_group_norm_fwd_workspace_bytes() (0 per token).
+ */
+kda_status kda_group_norm_fwd(const void* x, const float* weight, const float* bias,
+                              const int32_t* cu_seqlens, float eps,
+                              void* out, float* mean, float* rstd,
+                              int B, int T, int C, int G, int N, kda_dtype dtype, unsigned flags,
+                              void* workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t kda_group_norm_fwd_workspace_bytes(int B, int T, int C, int G, int N, int packed,
+                                          kda_dtype dtype, unsigned flags);
+
+/*
+ * kda_group_norm_bwd -- backward pass of kda_group_norm_fwd, from its inputs,
+ * the mean and rstd it wrote and d_out [B, T, C] (dtype).  Writes fp32 grad_x
+ * [B, T, C], and, each unless NULL, grad_weight and grad_bias [C].
+ */
+kda_status kda_group_norm_bwd(const void* x, const float* weight, const float* bias,
+                              const int32_t* cu_seqlens, const float* mean, const float* rstd,
+                              const void* d_out, float* grad_x, float* grad_weight,
+                              float* grad_bias,
+                              int B, int T, int C, int G, int N, kda_dtype dtype, unsigned flags,
+                              void* workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t kda_group_norm_bwd_workspace_bytes(int B, int T, int C, int G, int N, int packed,
+                                          kda_dtype dtype, unsigned flags);
 
 /*
  * kda_set_prefill_kernel -- which kernel the bf16 kda_chunk_fwd uses, for
