@@ -75,88 +75,112 @@ kda_norm_rows_kernel(const T* __restrict__ x, const float* __restrict__ weight, 
         }
     }
     const float inv = 1.f / (float)Cg;
+    constexpr int U = kBwd ? (NV == 1 ? 2 : 1) : 4 / NV;  // rows in flight per lane
     const long long steps = (rows + walkers - 1) / walkers;
-    for (long long s = 0; s < steps; ++s) {
-        const long long r = k + s * walkers;
-        const bool here = live && r < rows;
-        const size_t at = ((size_t)(here ? r : 0) * G + g) * Cg;
-        float v[NV][V];
+    for (long long s = 0; s < steps; s += U) {
+        Raw<T, V> rx[U][NV], rd[kBwd ? U : 1][kBwd ? NV : 1];
+        float ms[U], rss[U];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (lane + i * LANES) * V;
-            if (here && c < Cg) load_vec<V>(x + at + c, v[i]);
-            else
+        for (int q = 0; q < U; ++q) {
+            const long long r = k + (s + q) * walkers;
+            const bool here = live && r < rows;
+            const size_t at = ((size_t)r * G + g) * Cg;
 #pragma unroll
-                for (int j = 0; j < V; ++j) v[i][j] = 0.f;
+            for (int i = 0; i < NV; ++i) {
+                const int c = (lane + i * LANES) * V;
+                if (here && c < Cg) {
+                    rx[q][i].load(x + at + c);
+                    if constexpr (kBwd) rd[q][i].load(d_out + at + c);
+                }
+            }
+            if (kBwd) {
+                ms[q] = here ? mean[(size_t)r * G + g] : 0.f;
+                rss[q] = here ? rstd[(size_t)r * G + g] : 0.f;
+            }
         }
-        if constexpr (!kBwd) {
-            float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int j = 0; j < V; ++j) sum += v[i][j];
-            const float m = lane_sum<LANES>(sum) * inv;
-            float sq = 0.f;
+        for (int q = 0; q < U; ++q) {
+            const long long r = k + (s + q) * walkers;
+            const bool here = live && r < rows;
+            const size_t at = ((size_t)r * G + g) * Cg;
+            float v[NV][V];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (lane + i * LANES) * V;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float d = c < Cg ? v[i][j] - m : 0.f;
-                    sq = fmaf(d, d, sq);
-                }
-            }
-            const float rs = 1.f / sqrtf(fmaf(lane_sum<LANES>(sq), inv, eps));
-            if (!here) continue;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (lane + i * LANES) * V;
-                if (c >= Cg) continue;
-                float y[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    y[j] = fmaf((v[i][j] - m) * rs, w[i][j], b[i][j]);
-                    if (act) y[j] = silu(y[j]);
-                }
-                store_vec<V>(out + at + c, y);
-            }
-            if (lane == 0) {
-                mean[(size_t)r * G + g] = m;
-                rstd[(size_t)r * G + g] = rs;
-            }
-        } else {
-            const float m = here ? mean[(size_t)r * G + g] : 0.f, rs = here ? rstd[(size_t)r * G + g] : 0.f;
-            float dy[NV][V], s1 = 0.f, s2 = 0.f;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (lane + i * LANES) * V;
-                if (here && c < Cg) load_vec<V>(d_out + at + c, dy[i]);
+                if (here && c < Cg) rx[q][i].get(v[i]);
                 else
 #pragma unroll
-                    for (int j = 0; j < V; ++j) dy[i][j] = 0.f;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    v[i][j] = (v[i][j] - m) * rs;  // xhat
-                    if (act) dy[i][j] *= silu_slope(fmaf(v[i][j], w[i][j], b[i][j]));
-                    if (!here || c >= Cg) v[i][j] = dy[i][j] = 0.f;
-                    dw[i][j] = fmaf(dy[i][j], v[i][j], dw[i][j]);
-                    db[i][j] += dy[i][j];
-                    dy[i][j] *= w[i][j];
-                    s1 += dy[i][j];
-                    s2 = fmaf(dy[i][j], v[i][j], s2);
-                }
+                    for (int j = 0; j < V; ++j) v[i][j] = 0.f;
             }
-            s1 = lane_sum<LANES>(s1) * inv;
-            s2 = lane_sum<LANES>(s2) * inv;
-            if (!here) continue;
+            if constexpr (!kBwd) {
+                float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (lane + i * LANES) * V;
-                if (c >= Cg) continue;
-                float dx[V];
+                for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < V; ++j) dx[j] = rs * (dy[i][j] - s1 - v[i][j] * s2);
-                store_vec<V>(grad_x + at + c, dx);
+                    for (int j = 0; j < V; ++j) sum += v[i][j];
+                const float m = lane_sum<LANES>(sum) * inv;
+                float sq = 0.f;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int c = (lane + i * LANES) * V;
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const float d = c < Cg ? v[i][j] - m : 0.f;
+                        sq = fmaf(d, d, sq);
+                    }
+                }
+                const float rs = 1.f / sqrtf(fmaf(lane_sum<LANES>(sq), inv, eps));
+                if (!here) continue;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int c = (lane + i * LANES) * V;
+                    if (c >= Cg) continue;
+                    float y[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        y[j] = fmaf((v[i][j] - m) * rs, w[i][j], b[i][j]);
+                        if (act) y[j] = silu(y[j]);
+                    }
+                    store_vec<V>(out + at + c, y);
+                }
+                if (lane == 0) {
+                    mean[(size_t)r * G + g] = m;
+                    rstd[(size_t)r * G + g] = rs;
+                }
+            } else {
+                const float m = ms[q], rs = rss[q];
+                float dy[NV][V], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int c = (lane + i * LANES) * V;
+                    if (here && c < Cg) rd[q][i].get(dy[i]);
+                    else
+#pragma unroll
+                        for (int j = 0; j < V; ++j) dy[i][j] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        v[i][j] = (v[i][j] - m) * rs;  // xhat
+                        if (act) dy[i][j] *= silu_slope(fmaf(v[i][j], w[i][j], b[i][j]));
+                        if (!here || c >= Cg) v[i][j] = dy[i][j] = 0.f;
+                        dw[i][j] = fmaf(dy[i][j], v[i][j], dw[i][j]);
+                        db[i][j] += dy[i][j];
+                        dy[i][j] *= w[i][j];
+                        s1 += dy[i][j];
+                        s2 = fmaf(dy[i][j], v[i][j], s2);
+                    }
+                }
+                s1 = lane_sum<LANES>(s1) * inv;
+                s2 = lane_sum<LANES>(s2) * inv;
+                if (!here) continue;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int c = (lane + i * LANES) * V;
+                    if (c >= Cg) continue;
+                    float dx[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j) dx[j] = rs * (dy[i][j] - s1 - v[i][j] * s2);
+                    store_vec<V>(grad_x + at + c, dx);
+                }
             }
         }
     }
@@ -270,29 +294,55 @@ kda_norm_long_rows_kernel(const T* __restrict__ x, const float* __restrict__ wei
 
 // ---- over sequences ---------------------------------------------------------
 // A block takes one unit of tokens and `gb` whole groups.  Where gb groups fit
-// its 256 threads (cols = gb Cg / V columns), a thread keeps to one column and
+// 256 threads (cols = gb Cg / V columns), a thread keeps to one column and
 // strides over the tokens; a group wider than 256 columns has a block of its
 // own whose threads walk the columns too.
 struct Layout {
-    int cols, cpg, gb, ngb, ty;  // columns per block and per group, groups per block, blocks across, token lanes
+    int cols, cpg, gb, ngb, ty, threads;  // columns per block and per group, groups per block, blocks across, token lanes
+    int len;                              // tokens per unit
 };
 
-template <int V>
-Layout layout_of(int C, int G)
+// One unit's tokens of the column at p, ty apart, kBatch rows in flight.
+constexpr int kBatch = 8;
+template <typename T, int V, typename F>
+__device__ __forceinline__ void each_token(const T* p, long long a, long long b, int C, int ty, F&& f)
 {
-    Layout l;
-    l.cpg = C / G / V;
-    if (l.cpg >= 256) {
-        l.gb = 1;
-        l.cols = l.cpg;
-        l.ty = 1;
-    } else {
-        l.gb = 256 / l.cpg < G ? 256 / l.cpg : G;
-        l.cols = l.gb * l.cpg;
-        l.ty = 256 / l.cols;
+    for (long long t = a; t < b; t += (long long)kBatch * ty) {
+        Raw<T, V> r[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (t + i * ty < b) r[i].load(p + (size_t)(t + i * ty) * C);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (t + i * ty < b) {
+                float v[V];
+                r[i].get(v);
+                f(t + i * ty, v);
+            }
     }
-    l.ngb = (G + l.gb - 1) / l.gb;
-    return l;
+}
+// ... of the columns at p and q
+template <typename T, int V, typename F>
+__device__ __forceinline__ void each_token2(const T* p, const T* q, long long a, long long b, int C, int ty, F&& f)
+{
+    constexpr int U = kBatch / 2;
+    for (long long t = a; t < b; t += (long long)U * ty) {
+        Raw<T, V> r[U], s[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (t + i * ty < b) {
+                r[i].load(p + (size_t)(t + i * ty) * C);
+                s[i].load(q + (size_t)(t + i * ty) * C);
+            }
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (t + i * ty < b) {
+                float v[V], w[V];
+                r[i].get(v);
+                s[i].get(w);
+                f(t + i * ty, v, w);
+            }
+    }
 }
 
 // Partial statistics: part[(unit G + g) 2 ..] = mean and squared deviations of
@@ -312,28 +362,23 @@ kda_norm_stats_kernel(const T* __restrict__ x, float* __restrict__ part, Units u
     const int ty = wide ? 0 : threadIdx.x / l.cols;
     const int cx = wide ? threadIdx.x : threadIdx.x % l.cols;
     Moments mo = {0.f, 0.f, 0.f};
-    if (ty < l.ty && cx < groups * l.cpg) {
+    if (ty < l.ty && a + ty < b) {
         for (int c = cx; c < groups * l.cpg; c += wide ? 256 : l.cols) {
-            const T* p = x + (size_t)g0 * l.cpg * V + (size_t)c * V;
-            float k = 0.f, s1 = 0.f, s2 = 0.f;
-            long long cnt = 0;
-            for (long long t = a + ty; t < b; t += l.ty) {
-                float v[V];
-                load_vec<V>(p + (size_t)t * C, v);
-                if (cnt == 0) k = v[0];
+            const T* p = x + ((size_t)g0 * l.cpg + c) * V;
+            float first[V], s1 = 0.f, s2 = 0.f;
+            load_vec<V>(p + (size_t)(a + ty) * C, first);
+            const float k = first[0];
+            each_token<T, V>(p, a + ty, b, C, l.ty, [&](long long, const float (&v)[V]) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const float d = v[j] - k;
                     s1 += d;
                     s2 = fmaf(d, d, s2);
                 }
-                cnt += V;
-            }
-            if (cnt > 0) {
-                const float f = (float)cnt, d = s1 / f;
-                const Moments o = {f, k + d, fmaxf(s2 - s1 * d, 0.f)};
-                mo.merge(o);
-            }
+            });
+            const float cnt = (float)((b - a - ty + l.ty - 1) / l.ty * V), d = s1 / cnt;
+            const Moments o = {cnt, k + d, fmaxf(s2 - s1 * d, 0.f)};
+            mo.merge(o);
         }
     }
     sn[threadIdx.x] = mo.n;
@@ -342,7 +387,7 @@ kda_norm_stats_kernel(const T* __restrict__ x, float* __restrict__ part, Units u
     __syncthreads();
     // a warp per group: its threads' moments lane by lane, then across lanes
     const int lane = threadIdx.x & 31;
-    for (int g = threadIdx.x >> 5; g < groups; g += 8) {
+    for (int g = threadIdx.x >> 5; g < groups; g += l.threads / 32) {
         const int per = wide ? 256 : l.cpg * l.ty;
         Moments t = {0.f, 0.f, 0.f};
         for (int i = lane; i < per; i += 32) {
@@ -356,10 +401,7 @@ kda_norm_stats_kernel(const T* __restrict__ x, float* __restrict__ part, Units u
                                __shfl_xor_sync(0xffffffffu, t.q, o)};
             t.merge(u);
         }
-        if (lane == 0) {
-            part[((size_t)unit * G + g0 + g) * 2] = t.m;
-            part[((size_t)unit * G + g0 + g) * 2 + 1] = t.q;
-        }
+        if (lane == 0) *reinterpret_cast<float2*>(part + ((size_t)unit * G + g0 + g) * 2) = make_float2(t.m, t.q);
     }
 }
 
@@ -423,55 +465,61 @@ kda_norm_apply_kernel(const T* __restrict__ x, const float* __restrict__ weight,
             w[j] = weight ? weight[ch + j] : 1.f;
             bb[j] = bias ? bias[ch + j] : 0.f;
         }
-        const float k1 = kBwd ? sums[ng * 2] : 0.f, k2 = kBwd ? sums[ng * 2 + 1] : 0.f;
-#pragma unroll 4
-        for (long long t = a + ty; t < b; t += l.ty) {
-            const size_t at = (size_t)t * C + ch;
-            float v[V];
-            load_vec<V>(x + at, v);
-            if constexpr (!kBwd) {
+        if constexpr (!kBwd) {
+            each_token<T, V>(x + ch, a + ty, b, C, l.ty, [&](long long t, float (&v)[V]) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     v[j] = fmaf((v[j] - m) * rs, w[j], bb[j]);
                     if (act) v[j] = silu(v[j]);
                 }
-                store_vec<V>(out + at, v);
-            } else {
-                float dy[V];
-                load_vec<V>(d_out + at, dy);
+                store_vec<V>(out + (size_t)t * C + ch, v);
+            });
+        } else {
+            const float k1 = sums[ng * 2], k2 = sums[ng * 2 + 1];
+            each_token2<T, V>(x + ch, d_out + ch, a + ty, b, C, l.ty, [&](long long t, float (&v)[V], float (&dy)[V]) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const float xh = (v[j] - m) * rs;
                     if (act) dy[j] *= silu_slope(fmaf(xh, w[j], bb[j]));
                     dy[j] = rs * (dy[j] * w[j] - k1 - xh * k2);
                 }
-                store_vec<V>(grad_x + at, dy);
-            }
+                store_vec<V>(grad_x + (size_t)t * C + ch, dy);
+            });
         }
     }
 }
 
-// Backward sums of a unit: part[unit][0][c] = sum dv xhat, part[unit][1][c] = sum dv.
+// Backward sums of a unit: part[unit][0][c] = sum dv xhat, part[unit][1][c] =
+// sum dv, and over a group's channels gsum[(unit G + g) 2 ..] = sum k, sum k
+// xhat (k = dv w).  A slot without a unit gets zeros in `part`.
 template <typename T, int V>
 __global__ void __launch_bounds__(256)
 kda_norm_bwd_sums_kernel(const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
                          const float* __restrict__ mean, const float* __restrict__ rstd,
-                         const T* __restrict__ d_out, float* __restrict__ part, Units units, Layout l, int C, int G,
-                         int act)
+                         const T* __restrict__ d_out, float* __restrict__ part, float* __restrict__ gsum,
+                         Units units, Layout l, int C, int G, int act)
 {
-    __shared__ float red[2 * V * 256];
+    __shared__ float red[2 * V * 256];  // per thread, then [2][channels] of the block
     int n, seg;
     long long a, b;
     const long long unit = blockIdx.x / l.ngb;
-    if (!units.locate(unit, n, seg, a, b)) return;
     const int g0 = (int)(blockIdx.x % l.ngb) * l.gb;
     const int groups = G - g0 < l.gb ? G - g0 : l.gb;
     const int wide = l.cols > 256;
+    const int chans = groups * l.cpg * V, ch0 = g0 * l.cpg * V;
+    const int lane = threadIdx.x & 31;
+    float* pw = part + ((size_t)unit * 2) * C + ch0;
+    float* pb = pw + C;
+    if (!units.locate(unit, n, seg, a, b)) {
+        for (int c = threadIdx.x; c < chans; c += l.threads) pw[c] = pb[c] = 0.f;
+        return;
+    }
     const int ty = wide ? 0 : threadIdx.x / l.cols;
     const int cx = wide ? threadIdx.x : threadIdx.x % l.cols;
+    float s1 = 0.f, s2 = 0.f;
     for (int c = cx; c < groups * l.cpg; c += wide ? 256 : l.cols) {
         if (ty >= l.ty) break;
-        const int ch = (g0 * l.cpg + c) * V;
+        const int ch = ch0 + c * V;
         const size_t ng = (size_t)n * G + g0 + c / l.cpg;
         const float m = mean[ng], rs = rstd[ng];
         float w[V], bb[V], dw[V], db[V];
@@ -481,12 +529,7 @@ kda_norm_bwd_sums_kernel(const T* __restrict__ x, const float* __restrict__ weig
             bb[j] = bias ? bias[ch + j] : 0.f;
             dw[j] = db[j] = 0.f;
         }
-#pragma unroll 4
-        for (long long t = a + ty; t < b; t += l.ty) {
-            const size_t at = (size_t)t * C + ch;
-            float v[V], dy[V];
-            load_vec<V>(x + at, v);
-            load_vec<V>(d_out + at, dy);
+        each_token2<T, V>(x + ch, d_out + ch, a + ty, b, C, l.ty, [&](long long, float (&v)[V], float (&dy)[V]) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float xh = (v[j] - m) * rs;
@@ -494,10 +537,15 @@ kda_norm_bwd_sums_kernel(const T* __restrict__ x, const float* __restrict__ weig
                 dw[j] = fmaf(dy[j], xh, dw[j]);
                 db[j] += dy[j];
             }
-        }
+        });
         if (wide) {
-            store_vec<V>(part + ((size_t)unit * 2) * C + ch, dw);
-            store_vec<V>(part + ((size_t)unit * 2 + 1) * C + ch, db);
+            store_vec<V>(pw + c * V, dw);
+            store_vec<V>(pb + c * V, db);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                s1 = fmaf(w[j], db[j], s1);
+                s2 = fmaf(w[j], dw[j], s2);
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -506,106 +554,141 @@ kda_norm_bwd_sums_kernel(const T* __restrict__ x, const float* __restrict__ weig
             }
         }
     }
-    if (wide) return;  // the whole block agrees
+    if (wide) {  // the whole block agrees
+        s1 = block_sum(s1, red);
+        s2 = block_sum(s2, red + 8);
+        if (threadIdx.x == 0) {
+            gsum[((size_t)unit * G + g0) * 2] = s1;
+            gsum[((size_t)unit * G + g0) * 2 + 1] = s2;
+        }
+        return;
+    }
     __syncthreads();
-    for (int q = threadIdx.x; q < 2 * groups * l.cpg * V; q += 256) {
-        const int which = q / (groups * l.cpg * V), c = q - which * groups * l.cpg * V;
+    // a column's token lanes, into its first one's place
+    for (int q = threadIdx.x; q < 2 * V * l.cols; q += l.threads) {
+        const int which = q / l.cols, c = q - which * l.cols;
         float s = 0.f;
-        for (int y = 0; y < l.ty; ++y) s += red[(which * V + c % V) * 256 + y * l.cols + c / V];
-        part[((size_t)unit * 2 + which) * C + g0 * l.cpg * V + c] = s;
+        for (int y = 0; y < l.ty; ++y) s += red[which * 256 + y * l.cols + c];
+        red[which * 256 + c] = s;
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < chans; c += l.threads) {
+        pw[c] = red[(c % V) * 256 + c / V];
+        pb[c] = red[(V + c % V) * 256 + c / V];
+    }
+    for (int g = threadIdx.x >> 5; g < groups; g += l.threads / 32) {
+        float t1 = 0.f, t2 = 0.f;
+        for (int i = lane; i < l.cpg * V; i += 32) {
+            const int c = g * l.cpg * V + i;
+            const float w = weight ? weight[ch0 + c] : 1.f;
+            t1 = fmaf(w, red[(V + c % V) * 256 + c / V], t1);
+            t2 = fmaf(w, red[(c % V) * 256 + c / V], t2);
+        }
+        t1 = lane_sum<32>(t1);
+        t2 = lane_sum<32>(t2);
+        if (lane == 0) *reinterpret_cast<float2*>(gsum + ((size_t)unit * G + g0 + g) * 2) = make_float2(t1, t2);
     }
 }
 
-// From the units' sums: of every (sequence, group) the means of k = dv w and
-// k xhat, a warp each ...
-__global__ void __launch_bounds__(256)
-kda_norm_bwd_merge_kernel(const float* __restrict__ part, const float* __restrict__ weight,
-                          float* __restrict__ sums, Units units, int C, int G)
+// From the parts: the parameters' gradients (the first blocks; 32 channels
+// each, 32 lanes over the parts), and of every (sequence, group) the means of
+// k and k xhat (the others; a warp each).
+__global__ void __launch_bounds__(1024)
+kda_norm_bwd_merge_kernel(const float* __restrict__ part, float* __restrict__ grad_weight,
+                          float* __restrict__ grad_bias, long long parts, const float* __restrict__ gsum,
+                          float* __restrict__ sums, Units units, int C, int G, int param_blocks)
 {
-    const long long id = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
+    __shared__ float red[2][32][33];
+    const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
+    if ((int)blockIdx.x < param_blocks) {
+        const int c = blockIdx.x * 32 + lane;
+        float sw = 0.f, sb = 0.f;
+        if (c < C)
+#pragma unroll 4
+            for (long long i = y; i < parts; i += 32) {
+                sw += part[((size_t)i * 2) * C + c];
+                sb += part[((size_t)i * 2 + 1) * C + c];
+            }
+        red[0][y][lane] = sw;
+        red[1][y][lane] = sb;
+        __syncthreads();
+        if (y < 2 && c < C) {
+            float t = 0.f;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) t += red[y][k][lane];
+            if (y == 0 && grad_weight) grad_weight[c] = t;
+            if (y == 1 && grad_bias) grad_bias[c] = t;
+        }
+        return;
+    }
+    const long long id = (long long)(blockIdx.x - param_blocks) * 32 + y;
     if (id >= (long long)units.s.N * G) return;
-    const int n = (int)(id / G), g = (int)(id % G), Cg = C / G;
+    const int n = (int)(id / G), g = (int)(id % G);
     long long a, b;
     units.s.bounds(n, a, b);
     const long long first = units.first(n);
     const int cnt = units.count(n);
     float s1 = 0.f, s2 = 0.f;
-    for (long long i = lane; i < (long long)cnt * Cg; i += 32) {
-        const long long unit = first + i / Cg;
-        const int c = g * Cg + (int)(i % Cg);
-        const float w = weight ? weight[c] : 1.f;
-        s2 = fmaf(w, part[((size_t)unit * 2) * C + c], s2);
-        s1 = fmaf(w, part[((size_t)unit * 2 + 1) * C + c], s1);
+    for (int i = lane; i < cnt; i += 32) {
+        const float2 p = *reinterpret_cast<const float2*>(gsum + ((size_t)(first + i) * G + g) * 2);
+        s1 += p.x;
+        s2 += p.y;
     }
     s1 = lane_sum<32>(s1);
     s2 = lane_sum<32>(s2);
     if (lane == 0) {
-        const float inv = b > a ? 1.f / ((float)(b - a) * (float)Cg) : 0.f;
+        const float inv = b > a ? 1.f / ((float)(b - a) * (float)(C / G)) : 0.f;
         sums[id * 2] = s1 * inv;
         sums[id * 2 + 1] = s2 * inv;
     }
 }
 
-// ... and the parameters' gradients: 32 channels per block, eight lanes over
-// the parts.  Slots that no unit fills are passed over.
-__global__ void __launch_bounds__(256)
-kda_norm_params_kernel(const float* __restrict__ part, float* __restrict__ grad_weight,
-                       float* __restrict__ grad_bias, Units units, int by_unit, long long parts, int C)
-{
-    __shared__ float red[2][8][33];
-    const int lane = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-    float sw = 0.f, sb = 0.f;
-    for (long long i = y; i < parts; i += 8) {
-        if (by_unit) {
-            int n, seg;
-            long long a, b;
-            if (!units.locate(i, n, seg, a, b)) continue;
-        }
-        if (c < C) {
-            sw += part[((size_t)i * 2) * C + c];
-            sb += part[((size_t)i * 2 + 1) * C + c];
-        }
-    }
-    red[0][y][lane] = sw;
-    red[1][y][lane] = sb;
-    __syncthreads();
-    if (y < 2 && c < C) {
-        float t = 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) t += red[y][k][lane];
-        if (y == 0 && grad_weight) grad_weight[c] = t;
-        if (y == 1 && grad_bias) grad_bias[c] = t;
-    }
-}
-
 // ---- host -------------------------------------------------------------------
-
-constexpr int kUnitTokens = 64;
-
-Units units_of(const int32_t* cu, int packed, int B, int T, int N)
-{
-    Units u;
-    u.s.cu = cu;
-    u.s.N = N;
-    u.s.T = T;
-    u.s.total = (long long)B * T;
-    u.len = kUnitTokens;
-    u.per_seq = T > 0 ? (T + u.len - 1) / u.len : 1;
-    (void)packed;
-    return u;
-}
-long long slots_of(int B, int T, int N, int packed)
-{
-    return packed ? ((long long)B * T) / kUnitTokens + N
-                  : (long long)N * (T > 0 ? (T + kUnitTokens - 1) / kUnitTokens : 1);
-}
 
 // vector width: the widest of 8 (bf16 only), 4, 2 and 1 that divides a group
 int width_of(int Cg, kda_dtype dtype)
 {
     if (dtype == KDA_DTYPE_BF16 && Cg % 8 == 0) return 8;
     return Cg % 4 == 0 ? 4 : (Cg % 2 == 0 ? 2 : 1);
+}
+
+// Blocks of up to 256 threads; units of 8 to 64 tokens per thread, the longest
+// that still give every SM eight blocks.
+Layout layout_of(int C, int G, int V, long long tokens)
+{
+    Layout l;
+    l.cpg = C / G / V;
+    if (l.cpg > 256) {
+        l.gb = 1;
+        l.cols = l.cpg;
+        l.ty = 1;
+        l.threads = 256;
+    } else {
+        l.gb = 256 / l.cpg < G ? 256 / l.cpg : G;
+        l.cols = l.gb * l.cpg;
+        l.ty = 256 / l.cols;
+        l.threads = (l.cols * l.ty + 31) / 32 * 32;
+    }
+    l.ngb = (G + l.gb - 1) / l.gb;
+    l.len = 64 * l.ty;
+    while (l.len > 8 * l.ty && tokens / l.len * l.ngb < 8LL * sm_count()) l.len >>= 1;
+    return l;
+}
+
+Units units_of(const int32_t* cu, int B, int T, int N, int len)
+{
+    Units u;
+    u.s.cu = cu;
+    u.s.N = N;
+    u.s.T = T;
+    u.s.total = (long long)B * T;
+    u.len = len;
+    u.per_seq = T > 0 ? (T + len - 1) / len : 1;
+    return u;
+}
+long long slots_of(int B, int T, int N, int packed, int len)
+{
+    return packed ? ((long long)B * T) / len + N : (long long)N * (T > 0 ? (T + len - 1) / len : 1);
 }
 
 // Lanes per row and vectors per lane of the per-token kernel; lanes = 0: rows
@@ -679,60 +762,72 @@ cudaError_t forward(const NormArgs& a, kda_dtype dtype, cudaStream_t st)
         if ((long long)a.B * a.T == 0) return cudaSuccess;
         return rows<T, V, false>(a, row_shape((long long)a.B * a.T, a.C, a.G, dtype, false), st);
     }
-    const Units u = units_of(a.cu_seqlens, a.cu_seqlens != nullptr, a.B, a.T, a.N);
-    const Layout l = layout_of<V>(a.C, a.G);
-    const long long blocks = u.slots() * l.ngb;
-    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    const Layout l = layout_of(a.C, a.G, V, (long long)a.B * a.T);
+    const Units u = units_of(a.cu_seqlens, a.B, a.T, a.N, l.len);
+    const long long blocks = u.slots() * l.ngb, ng = (long long)a.N * a.G;
+    if (blocks > INT32_MAX || (ng + 7) / 8 > INT32_MAX) return cudaErrorInvalidConfiguration;
     float* part = (float*)a.workspace;
     if (blocks > 0) {
-        kda_norm_stats_kernel<T, V><<<(unsigned)blocks, 256, 0, st>>>((const T*)a.x, part, u, l, a.C, a.G);
+        kda_norm_stats_kernel<T, V><<<(unsigned)blocks, l.threads, 0, st>>>((const T*)a.x, part, u, l, a.C, a.G);
         if (cudaError_t e = cudaGetLastError()) return e;
     }
-    const long long ng = (long long)a.N * a.G;
     kda_norm_merge_kernel<<<(unsigned)((ng + 7) / 8), 256, 0, st>>>(part, a.mean, a.rstd, u, a.G, a.C / a.G, a.eps);
     if (cudaError_t e = cudaGetLastError()) return e;
     if (blocks > 0)
-        kda_norm_apply_kernel<T, V, false><<<(unsigned)blocks, 256, 0, st>>>(
+        kda_norm_apply_kernel<T, V, false><<<(unsigned)blocks, l.threads, 0, st>>>(
             (const T*)a.x, a.weight, a.bias, (T*)a.out, a.mean, a.rstd, nullptr, nullptr, nullptr, u, l, a.C, a.G,
             a.silu);
     return cudaGetLastError();
 }
 
+// The backward pass's workspace over sequences: the units' sums per channel
+// and per group, and the sequences'.
+struct SumSpace {
+    size_t part, gsum, sums, total;  // in floats
+};
+SumSpace sum_space(size_t slots, int C, int G, int N)
+{
+    SumSpace s;
+    s.part = 0;
+    s.gsum = slots * 2 * C;
+    s.sums = s.gsum + slots * 2 * G;
+    s.total = s.sums + (size_t)N * G * 2;
+    return s;
+}
+
 template <typename T, int V>
 cudaError_t backward(const NormArgs& a, kda_dtype dtype, cudaStream_t st)
 {
-    const long long tokens = (long long)a.B * a.T;
-    const unsigned pblocks = (unsigned)((a.C + 31) / 32);
+    const long long tokens = (long long)a.B * a.T, ng = (long long)a.N * a.G;
+    const int pblocks = (a.C + 31) / 32;
     float* part = (float*)a.workspace;
-    Units u = units_of(a.cu_seqlens, a.cu_seqlens != nullptr, a.B, a.T, a.N);
     if (a.per_token) {
         const RowShape r = row_shape(tokens, a.C, a.G, dtype, true);
         if (tokens > 0)
             if (cudaError_t e = rows<T, V, true>(a, r, st)) return e;
-        kda_norm_params_kernel<<<pblocks, 256, 0, st>>>(part, a.grad_weight, a.grad_bias, u, 0,
-                                                        tokens > 0 ? r.walkers : 0, a.C);
+        kda_norm_bwd_merge_kernel<<<(unsigned)pblocks, 1024, 0, st>>>(part, a.grad_weight, a.grad_bias,
+                                                                      tokens > 0 ? r.walkers : 0, nullptr, nullptr,
+                                                                      Units{}, a.C, a.G, pblocks);
         return cudaGetLastError();
     }
-    const Layout l = layout_of<V>(a.C, a.G);
-    const long long slots = u.slots(), blocks = slots * l.ngb;
-    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-    float* sums = part + (size_t)slots * 2 * a.C;
+    const Layout l = layout_of(a.C, a.G, V, tokens);
+    const Units u = units_of(a.cu_seqlens, a.B, a.T, a.N, l.len);
+    const long long slots = u.slots(), blocks = slots * l.ngb, mblocks = pblocks + (ng + 31) / 32;
+    if (blocks > INT32_MAX || mblocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    const SumSpace s = sum_space((size_t)slots, a.C, a.G, a.N);
     if (blocks > 0) {
-        kda_norm_bwd_sums_kernel<T, V><<<(unsigned)blocks, 256, 0, st>>>(
-            (const T*)a.x, a.weight, a.bias, a.mean, a.rstd, (const T*)a.d_out, part, u, l, a.C, a.G, a.silu);
+        kda_norm_bwd_sums_kernel<T, V><<<(unsigned)blocks, l.threads, 0, st>>>(
+            (const T*)a.x, a.weight, a.bias, a.mean, a.rstd, (const T*)a.d_out, part, part + s.gsum, u, l, a.C, a.G,
+            a.silu);
         if (cudaError_t e = cudaGetLastError()) return e;
     }
-    const long long ng = (long long)a.N * a.G;
-    if (ng > 0) {
-        kda_norm_bwd_merge_kernel<<<(unsigned)((ng + 7) / 8), 256, 0, st>>>(part, a.weight, sums, u, a.C, a.G);
-        if (cudaError_t e = cudaGetLastError()) return e;
-    }
-    kda_norm_params_kernel<<<pblocks, 256, 0, st>>>(part, a.grad_weight, a.grad_bias, u, 1, slots, a.C);
+    kda_norm_bwd_merge_kernel<<<(unsigned)mblocks, 1024, 0, st>>>(part, a.grad_weight, a.grad_bias, slots,
+                                                                  part + s.gsum, part + s.sums, u, a.C, a.G, pblocks);
     if (cudaError_t e = cudaGetLastError()) return e;
     if (blocks > 0)
-        kda_norm_apply_kernel<T, V, true><<<(unsigned)blocks, 256, 0, st>>>(
-            (const T*)a.x, a.weight, a.bias, nullptr, a.mean, a.rstd, (const T*)a.d_out, sums, a.grad_x, u, l, a.C,
-            a.G, a.silu);
+        kda_norm_apply_kernel<T, V, true><<<(unsigned)blocks, l.threads, 0, st>>>(
+            (const T*)a.x, a.weight, a.bias, nullptr, a.mean, a.rstd, (const T*)a.d_out, part + s.sums, a.grad_x, u,
+            l, a.C, a.G, a.silu);
     return cudaGetLastError();
 }
 
@@ -758,10 +853,11 @@ cudaError_t dispatch(const NormArgs& a, kda_dtype dtype, bool bwd, cudaStream_t 
 
 }  // namespace
 
-size_t norm_fwd_workspace(int B, int T, int, int G, int N, int per_token, int packed, kda_dtype)
+size_t norm_fwd_workspace(int B, int T, int C, int G, int N, int per_token, int packed, kda_dtype dtype)
 {
     if (per_token) return 0;
-    return (size_t)slots_of(B, T, N, packed) * G * 2 * sizeof(float);
+    const Layout l = layout_of(C, G, width_of(C / G, dtype), (long long)B * T);
+    return (size_t)slots_of(B, T, N, packed, l.len) * G * 2 * sizeof(float);
 }
 
 size_t norm_bwd_workspace(int B, int T, int C, int G, int N, int per_token, int packed, kda_dtype dtype)
@@ -770,7 +866,8 @@ size_t norm_bwd_workspace(int B, int T, int C, int G, int N, int per_token, int 
         if ((long long)B * T == 0) return 0;
         return (size_t)row_shape((long long)B * T, C, G, dtype, true).walkers * 2 * C * sizeof(float);
     }
-    return (size_t)slots_of(B, T, N, packed) * 2 * C * sizeof(float) + (size_t)N * G * 2 * sizeof(float);
+    const Layout l = layout_of(C, G, width_of(C / G, dtype), (long long)B * T);
+    return sum_space((size_t)slots_of(B, T, N, packed, l.len), C, G, N).total * sizeof(float);
 }
 
 cudaError_t launch_norm_fwd(const NormArgs& a, kda_dtype dtype, cudaStream_t st) { return dispatch(a, dtype, false, st); }

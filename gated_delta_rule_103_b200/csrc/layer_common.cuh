@@ -81,6 +81,22 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&x)[V])
     }
 }
 
+// V values as they lie in memory: loads that stay in flight in as few registers
+// as the type allows.
+template <typename T, int V>
+struct Raw {
+    alignas(sizeof(T) * V) T v[V];
+    __device__ __forceinline__ void load(const T* p)
+    {
+        constexpr int N = (int)sizeof(T) * V;
+        if constexpr (N == 16) *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
+        else if constexpr (N == 8) *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(p);
+        else if constexpr (N == 4) *reinterpret_cast<uint32_t*>(v) = *reinterpret_cast<const uint32_t*>(p);
+        else v[0] = p[0];
+    }
+    __device__ __forceinline__ void get(float (&x)[V]) const { load_vec<V>(v, x); }
+};
+
 // 1 / (1 + e^-x) with the fast exponential and reciprocal (relative error of
 // some 2^-22: below the rounding of the products it enters).  e^-x = inf
 // gives 0.

@@ -134,16 +134,24 @@ kda_short_conv_kernel(const T* __restrict__ x, const float* __restrict__ weight,
         float h[W - 1][V];
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) load_vec<V>(x + (size_t)(t - (W - 1) + j) * C + c0, h[j]);
-        constexpr int U = 8;  // rows in flight per thread
-        for (; t + U <= stop; t += U) {
-            float cur[U][V];
+        constexpr int U = 4;  // rows per batch; the next batch is in flight meanwhile
+        Raw<T, V> next[U];
+        if (t + U <= stop)
 #pragma unroll
-            for (int k = 0; k < U; ++k) load_vec<V>(x + (size_t)(t + k) * C + c0, cur[k]);
+            for (int k = 0; k < U; ++k) next[k].load(x + (size_t)(t + k) * C + c0);
+        for (; t + U <= stop; t += U) {
+            Raw<T, V> now[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) now[k] = next[k];
+            if (t + 2 * U <= stop)
+#pragma unroll
+                for (int k = 0; k < U; ++k) next[k].load(x + (size_t)(t + U + k) * C + c0);
 #pragma unroll
             for (int k = 0; k < U; ++k) {
-                float v[V];
-                taps.dot(h, cur[k], v);
-                push<W, V>(h, cur[k]);
+                float cur[V], v[V];
+                now[k].get(cur);
+                taps.dot(h, cur, v);
+                push<W, V>(h, cur);
                 if (act) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) v[i] = silu(v[i]);
@@ -197,12 +205,13 @@ kda_short_conv_step_kernel(const T* __restrict__ x, const float* __restrict__ we
 // Backward.  With dv = dy act'(v):
 //     dx[p]   = sum_j w[j] dv[p + W - 1 - j]  (+ the final state's adjoint on the last W - 1 rows)
 //     dw[j]   = sum_t dv[t] x[t - W + 1 + j],   dbias = sum_t dv[t]
-// A thread walks its run of tokens and the W - 1 behind it, with W - 1 rows of
-// x and W of dv in registers; v is computed again from x.  The parameters'
+// A thread walks its run of tokens and the W - 1 behind it, with the
+// last W - 1 rows of x and the unfinished rows of dx in registers; v is
+// computed again from x.  The parameters'
 // sums over a block's tokens go to `part` [tile][W + 1][C] and are added up by
 // the kernel below in a fixed order.
 template <typename T, int W, int V>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 2)
 kda_short_conv_bwd_kernel(const T* __restrict__ x, const float* __restrict__ weight,
                           const float* __restrict__ bias, const T* __restrict__ state,
                           const T* __restrict__ d_out, const float* __restrict__ d_fin,
@@ -267,35 +276,38 @@ kda_short_conv_bwd_kernel(const T* __restrict__ x, const float* __restrict__ wei
             const long long stop = b < end ? b : end;
             if (t0 < a) t0 = a;
             if (t0 >= stop) continue;
-            float h[W - 1][V], g[W][V];
+            float h[W - 1][V], part_dx[W - 1][V];  // part_dx[i]: what row t - (W - 1) + i has so far
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) ext_row<T, W, V>(x, state, n, a, t0 - a + j, C, c0, h[j]);
+            for (int j = 0; j < W - 1; ++j) {
+                ext_row<T, W, V>(x, state, n, a, t0 - a + j, C, c0, h[j]);
 #pragma unroll
-            for (int j = 0; j < W; ++j)
-#pragma unroll
-                for (int i = 0; i < V; ++i) g[j][i] = 0.f;
+                for (int i = 0; i < V; ++i) part_dx[j][i] = 0.f;
+            }
             constexpr int U = 4;  // rows of x and of dy in flight per thread
             for (long long t = t0; t < stop + W - 1; t += U) {
-                float cur[U][V], dy[U][V];
+                Raw<T, V> rx[U], rd[U];
 #pragma unroll
-                for (int k = 0; k < U; ++k) {
+                for (int k = 0; k < U; ++k)
                     if (t + k < b && t + k < stop + W - 1) {
-                        load_vec<V>(x + (size_t)(t + k) * C + c0, cur[k]);
-                        load_vec<V>(d_out + (size_t)(t + k) * C + c0, dy[k]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) cur[k][i] = dy[k][i] = 0.f;
+                        rx[k].load(x + (size_t)(t + k) * C + c0);
+                        rd[k].load(d_out + (size_t)(t + k) * C + c0);
                     }
-                }
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
                     if (t + k >= stop + W - 1) break;
-                    float v[V], dv[V];
-                    taps.dot(h, cur[k], v);
+                    float cur[V], v[V], dv[V];
+                    if (t + k < b) {
+                        rx[k].get(cur);
+                        rd[k].get(dv);
+                        taps.dot(h, cur, v);
+                        if (act) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        // rows behind the sequence have no adjoint, whatever v is there
-                        dv[i] = t + k < b ? (act ? dy[k][i] * silu_slope(v[i]) : dy[k][i]) : 0.f;
+                            for (int i = 0; i < V; ++i) dv[i] *= silu_slope(v[i]);
+                        }
+                    } else {
+                        // rows behind the sequence have no adjoint
+#pragma unroll
+                        for (int i = 0; i < V; ++i) cur[i] = dv[i] = 0.f;
                     }
                     if (t + k < stop) {
 #pragma unroll
@@ -303,25 +315,20 @@ kda_short_conv_bwd_kernel(const T* __restrict__ x, const float* __restrict__ wei
                             db[i] += dv[i];
 #pragma unroll
                             for (int j = 0; j < W - 1; ++j) dw[j][i] = fmaf(dv[i], h[j][i], dw[j][i]);
-                            dw[W - 1][i] = fmaf(dv[i], cur[k][i], dw[W - 1][i]);
+                            dw[W - 1][i] = fmaf(dv[i], cur[i], dw[W - 1][i]);
                         }
                     }
-                    push<W, V>(h, cur[k]);
+                    push<W, V>(h, cur);
+                    float dx[V];
 #pragma unroll
-                    for (int j = 0; j + 1 < W; ++j)
+                    for (int i = 0; i < V; ++i) {
+                        dx[i] = fmaf(taps.w[0][i], dv[i], part_dx[0][i]);
 #pragma unroll
-                        for (int i = 0; i < V; ++i) g[j][i] = g[j + 1][i];
-#pragma unroll
-                    for (int i = 0; i < V; ++i) g[W - 1][i] = dv[i];
+                        for (int j = 0; j + 1 < W - 1; ++j) part_dx[j][i] = fmaf(taps.w[j + 1][i], dv[i], part_dx[j + 1][i]);
+                        part_dx[W - 2][i] = taps.w[W - 1][i] * dv[i];
+                    }
                     const long long p = t + k - (W - 1);
                     if (p >= t0) {
-                        float dx[V];
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            dx[i] = 0.f;
-#pragma unroll
-                            for (int j = 0; j < W; ++j) dx[i] = fmaf(taps.w[j][i], g[W - 1 - j][i], dx[i]);
-                        }
                         const long long r = p - b + (W - 1);  // row of the final state
                         if (r >= 0 && d_fin) {
                             float f[V];

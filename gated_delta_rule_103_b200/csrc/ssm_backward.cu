@@ -119,15 +119,16 @@ kda_ssm_bwd_carry_kernel(BwdParams<T> p)
     const int ch = tid / L, s0 = (tid % L) * 4;
     const bool chan = ch < nch;
     const size_t row = (size_t)(c0 + (chan ? ch : 0)) * p.f.S;
-    float A[4], h[4], P[4], R[4], bias[4], dt_sum[4];
+    float A[4], bias[4], dt_sum[4];
     const int q4 = (tid % Q) * 4;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         A[i] = chan && s0 + i < p.f.S ? p.f.A[row + s0 + i] * kLog2e : 0.f;
-        h[i] = R[i] = dt_sum[i] = 0.f;
-        P[i] = 1.f;
+        dt_sum[i] = 0.f;
         bias[i] = p.f.delta_bias && q4 + i < nch ? p.f.delta_bias[c0 + q4 + i] : 0.f;
     }
+    const float2 A01 = make_float2(A[0], A[1]), A23 = make_float2(A[2], A[3]);
+    float2 h01 = both(0.f), h23 = h01, R01 = h01, R23 = h01, P01 = both(1.f), P23 = P01;
     Feed<T, Tl, true> feed;
     feed.fetch(p, t0, end, c0, nch, g, tid);
     feed.stage(p, t0, end, bias, s_e, s_B, s_C, dt_sum, tid);
@@ -143,19 +144,20 @@ kda_ssm_bwd_carry_kernel(BwdParams<T> p)
 #pragma unroll 4
         for (int j = 0; j < TT; ++j) {
             const float4 e = *reinterpret_cast<const float4*>(&s_e[(buf * TT + j) * CH + ch]);
-            const float4 B4 = *reinterpret_cast<const float4*>(&s_B[(buf * TT + j) * SP + s0]);
-            const float4 C4 = *reinterpret_cast<const float4*>(&s_C[(buf * TT + j) * SP + s0]);
-            const float B[4] = {B4.x, B4.y, B4.z, B4.w}, C[4] = {C4.x, C4.y, C4.z, C4.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float a = ex2(e.x * A[i]);
-                h[i] = fmaf(a, h[i], e.y * B[i]);
-                P[i] *= a;
-                R[i] = fmaf(P[i], e.z * C[i], R[i]);
-            }
+            const float4 B = *reinterpret_cast<const float4*>(&s_B[(buf * TT + j) * SP + s0]);
+            const float4 C = *reinterpret_cast<const float4*>(&s_C[(buf * TT + j) * SP + s0]);
+            const float2 dt = both(e.x), du = both(e.y), dy = both(e.z);
+            const float2 a01 = ex2(mul2(dt, A01)), a23 = ex2(mul2(dt, A23));
+            h01 = fma2(a01, h01, mul2(du, make_float2(B.x, B.y)));
+            h23 = fma2(a23, h23, mul2(du, make_float2(B.z, B.w)));
+            P01 = mul2(P01, a01);
+            P23 = mul2(P23, a23);
+            R01 = fma2(P01, mul2(dy, make_float2(C.x, C.y)), R01);
+            R23 = fma2(P23, mul2(dy, make_float2(C.z, C.w)), R23);
         }
         __syncthreads();
     }
+    const float h[4] = {h01.x, h01.y, h23.x, h23.y}, R[4] = {R01.x, R01.y, R23.x, R23.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (chan && s0 + i < p.f.S) {
@@ -214,13 +216,14 @@ template <typename T, int L>
 constexpr size_t bwd_smem()
 {
     using Tl = BTile<L>;
-    // staged operands, results per (token, channel), warps' sums of dB and dC
+    // staged operands, results per (token, channel), warps' sums of dB and dC,
+    // entry states of every four tokens
     return sizeof(float) * (2 * Tl::TT * Tl::CH * 4 + 4 * Tl::TT * Tl::SP + 3 * Tl::TT * Tl::YP +
-                            (kThreads / 32) * Tl::TT * 2 * Tl::SP);
+                            (kThreads / 32) * Tl::TT * 2 * Tl::SP + Tl::TT * kThreads);
 }
 
 template <typename T, int L>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 kda_ssm_bwd_kernel(BwdParams<T> p)
 {
     using Tl = BTile<L>;
@@ -232,6 +235,7 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
     float* s_C = s_B + 2 * TT * SP;                                 // [2][TT][SP]
     float* s_o = s_C + 2 * TT * SP;                                 // [3][TT][YP]: g.B, sum g a h A, C.h
     float* s_w = s_o + 3 * TT * YP;                                 // [WARPS][TT][2][SP]
+    float4* s_m = reinterpret_cast<float4*>(s_w + WARPS * TT * 2 * SP);  // [TT / 4][threads]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int D = p.f.D, S = p.f.S;
     const int across = p.f.G * p.f.cpb;
@@ -259,14 +263,14 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
     const long long tile0 = t0 / TT + slot;
     const int tiles = (int)((end - t0 + TT - 1) / TT);
 
-    float A[4], h[4], c[4], dA[4], bias[4], skip[4];
+    float A[4], h[4], c[4], bias[4], skip[4];
     const int q4 = (tid % Q) * 4;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const bool ok = chan && s0 + i < S;
         const size_t at = row + s0 + i;
         A[i] = ok ? p.f.A[at] * kLog2e : 0.f;
-        h[i] = c[i] = dA[i] = 0.f;
+        h[i] = c[i] = 0.f;
         if (ok) {
             if (p.f.ends && seg > 0) h[i] = p.f.ends[(size_t)slot * DS + at];
             else if (p.f.init) h[i] = p.f.init[(size_t)n * DS + at];
@@ -276,6 +280,18 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
         bias[i] = p.f.delta_bias && q4 + i < nch ? p.f.delta_bias[c0 + q4 + i] : 0.f;
         skip[i] = p.f.skip && q4 + i < nch ? p.f.skip[c0 + q4 + i] : 0.f;
     }
+
+    const float2 A01 = make_float2(A[0], A[1]), A23 = make_float2(A[2], A[3]);
+    float2 h01 = make_float2(h[0], h[1]), h23 = make_float2(h[2], h[3]);
+    float2 c01 = make_float2(c[0], c[1]), c23 = make_float2(c[2], c[3]);
+    float2 dA01 = both(0.f), dA23 = dA01;
+    auto advance = [&](int j, float2& x01, float2& x23) {
+        const float2 dd = *reinterpret_cast<const float2*>(&s_e[j * CH + ch]);
+        const float4 B = *reinterpret_cast<const float4*>(&s_B[j * SP + s0]);
+        const float2 dt = both(dd.x), du = both(dd.y);
+        x01 = fma2(ex2(mul2(dt, A01)), x01, mul2(du, make_float2(B.x, B.y)));
+        x23 = fma2(ex2(mul2(dt, A23)), x23, mul2(du, make_float2(B.z, B.w)));
+    };
 
     // forward: the state at every tile's entry
     {
@@ -294,44 +310,108 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
             }
             float* e = p.entries + (size_t)(tile0 + k) * DS + row + s0;
             if (chan) {
-                if (p.f.vec_s) {
-                    if (s0 < S) *reinterpret_cast<float4*>(e) = make_float4(h[0], h[1], h[2], h[3]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (s0 + i < S) e[i] = h[i];
-                }
+                const float x[4] = {h01.x, h01.y, h23.x, h23.y};
+                store4(e, x, p.f.vec_s && s0 < S, S - s0);
             }
-            if (k + 1 < tiles) {
+            if (k + 1 < tiles)
 #pragma unroll 4
-                for (int j = 0; j < TT; ++j) {
-                    const float2 dd = *reinterpret_cast<const float2*>(&s_e[(buf * TT + j) * CH + ch]);
-                    const float4 B4 = *reinterpret_cast<const float4*>(&s_B[(buf * TT + j) * SP + s0]);
-                    h[0] = fmaf(ex2(dd.x * A[0]), h[0], dd.y * B4.x);
-                    h[1] = fmaf(ex2(dd.x * A[1]), h[1], dd.y * B4.y);
-                    h[2] = fmaf(ex2(dd.x * A[2]), h[2], dd.y * B4.z);
-                    h[3] = fmaf(ex2(dd.x * A[3]), h[3], dd.y * B4.w);
-                }
-            }
+                for (int j = 0; j < TT; ++j) advance(buf * TT + j, h01, h23);
             __syncthreads();
         }
     }
 
     // backward, from the last tile (its entry state is in h) to the first
     Feed<T, Tl, true> feed;
-    ChannelRows<T, Tl> u_now, d_now, z_now, o_now;
     float sum_skip[4] = {0.f, 0.f, 0.f, 0.f}, sum_bias[4] = {0.f, 0.f, 0.f, 0.f};
     if (tiles > 0) feed.fetch(p, t0 + (long long)(tiles - 1) * TT, end, c0, nch, g, tid);
     for (int k = tiles - 1; k >= 0; --k) {
         const long long t = t0 + (long long)k * TT;
         feed.stage(p, t, end, bias, s_e, s_B, s_C, nullptr, tid);
-        u_now = feed.u;
-        d_now = feed.d;
-        o_now = feed.o;
-        if (p.f.z) z_now = feed.z;
-        float next[4] = {0.f, 0.f, 0.f, 0.f};
+        __syncthreads();
+        // The tile goes by in fours: their entry states first (each thread's own
+        // in shared memory), then from the last four to the first their states
+        // and decays again, held in registers.
+#pragma unroll 1
+        for (int q = 0; q < TT / 4; ++q) {
+            s_m[q * kThreads + tid] = make_float4(h01.x, h01.y, h23.x, h23.y);
+            if (q + 1 < TT / 4)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) advance(q * 4 + j, h01, h23);
+        }
+        float2 dA01_t = both(0.f), dA23_t = dA01_t;
+#pragma unroll 1
+        for (int tb = TT - 4; tb >= 0; tb -= 4) {
+            const float4 m = s_m[tb / 4 * kThreads + tid];
+            const float2 b01 = make_float2(m.x, m.y), b23 = make_float2(m.z, m.w);
+            float2 hs[4][2], as[4][2];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 dd = *reinterpret_cast<const float2*>(&s_e[(tb + j) * CH + ch]);
+                const float4 B = *reinterpret_cast<const float4*>(&s_B[(tb + j) * SP + s0]);
+                const float2 dt = both(dd.x), du = both(dd.y);
+                as[j][0] = ex2(mul2(dt, A01));
+                as[j][1] = ex2(mul2(dt, A23));
+                hs[j][0] = fma2(as[j][0], j ? hs[j > 0 ? j - 1 : 0][0] : b01, mul2(du, make_float2(B.x, B.y)));
+                hs[j][1] = fma2(as[j][1], j ? hs[j > 0 ? j - 1 : 0][1] : b23, mul2(du, make_float2(B.z, B.w)));
+            }
+            float o[3][4];  // [what][token]
+#pragma unroll
+            for (int jj = 3; jj >= 0; --jj) {
+                const int tok = tb + jj;
+                const float4 e = *reinterpret_cast<const float4*>(&s_e[tok * CH + ch]);
+                const float4 B = *reinterpret_cast<const float4*>(&s_B[tok * SP + s0]);
+                const float4 C = *reinterpret_cast<const float4*>(&s_C[tok * SP + s0]);
+                const float2 dt = both(e.x), du = both(e.y), dy = both(e.z);
+                const float2 B01 = make_float2(B.x, B.y), B23 = make_float2(B.z, B.w);
+                const float2 C01 = make_float2(C.x, C.y), C23 = make_float2(C.z, C.w);
+                const float2 g01 = fma2(C01, dy, c01), g23 = fma2(C23, dy, c23);
+                c01 = mul2(as[jj][0], g01);
+                c23 = mul2(as[jj][1], g23);
+                const float2 w01 = mul2(c01, jj ? hs[jj > 0 ? jj - 1 : 0][0] : b01);
+                const float2 w23 = mul2(c23, jj ? hs[jj > 0 ? jj - 1 : 0][1] : b23);
+                dA01_t = fma2(w01, dt, dA01_t);
+                dA23_t = fma2(w23, dt, dA23_t);
+                const float2 gB = fma2(g01, B01, mul2(g23, B23));
+                const float2 wA = fma2(w01, A01, mul2(w23, A23));
+                const float2 hC = fma2(hs[jj][0], C01, mul2(hs[jj][1], C23));
+                o[0][jj] = gB.x + gB.y;
+                o[1][jj] = wA.x + wA.y;
+                o[2][jj] = hC.x + hC.y;
+                const float2 p0 = mul2(g01, du), p1 = mul2(g23, du);
+                const float2 p2 = mul2(hs[jj][0], dy), p3 = mul2(hs[jj][1], dy);
+                float bc[8] = {p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
+                fold<8, NL, L>(bc, lane);
+                constexpr int KEEP = NL >= 8 ? 1 : 8 / NL;
+                constexpr int BITS = NL >= 8 ? 3 : (NL == 4 ? 2 : (NL == 2 ? 1 : 0));
+                if (lane / L < 8) {
+                    const int at = fold_index<BITS>(lane, L) * KEEP;  // of {B: 0..3, C: 4..7}
+#pragma unroll
+                    for (int i = 0; i < KEEP; ++i) {
+                        const int v = at + i;
+                        s_w[((warp * TT + tok) * 2 + (v >> 2)) * SP + s0 + (v & 3)] = bc[i];
+                    }
+                }
+            }
+            constexpr int KEEP = L >= 4 ? 1 : 4 / L;
+            constexpr int BITS = L >= 4 ? 2 : (L == 2 ? 1 : 0);
+#pragma unroll
+            for (int w = 0; w < 3; ++w) {
+                if (w == 2 && !p.f.z) break;  // y is wanted for dz alone
+                fold<4, L, 1>(o[w], lane);
+                if (tid % L < 4) {
+                    const int at = tb + fold_index<BITS>(lane, 1) * KEEP;
+#pragma unroll
+                    for (int i = 0; i < KEEP; ++i) s_o[(w * TT + at + i) * YP + ch] = o[w][i];
+                }
+            }
+        }
+        // a tile's sum first: long sums of small terms keep their digits
+        dA01.x += dA01_t.x;
+        dA01.y += dA01_t.y;
+        dA23.x += dA23_t.x;
+        dA23.y += dA23_t.y;
         if (k > 0) {
-            feed.fetch(p, t - TT, end, c0, nch, g, tid);
+            float next[4] = {0.f, 0.f, 0.f, 0.f};
             const float* e = p.entries + (size_t)(tile0 + k - 1) * DS + row + s0;
             if (chan) {
                 if (p.f.vec_s) {
@@ -342,70 +422,9 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
                         if (s0 + i < S) next[i] = e[i];
                 }
             }
+            h01 = make_float2(next[0], next[1]);
+            h23 = make_float2(next[2], next[3]);
         }
-        __syncthreads();
-        float hs[TT][4];
-#pragma unroll
-        for (int j = 0; j < TT; ++j) {
-            const float2 dd = *reinterpret_cast<const float2*>(&s_e[j * CH + ch]);
-            const float4 B4 = *reinterpret_cast<const float4*>(&s_B[j * SP + s0]);
-            const float B[4] = {B4.x, B4.y, B4.z, B4.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                hs[j][i] = fmaf(ex2(dd.x * A[i]), j ? hs[j > 0 ? j - 1 : 0][i] : h[i], dd.y * B[i]);
-        }
-#pragma unroll
-        for (int jb = TT - 4; jb >= 0; jb -= 4) {
-            float o[3][4];  // [what][token]
-#pragma unroll
-            for (int jj = 3; jj >= 0; --jj) {
-                const int j = jb + jj;
-                const float4 e = *reinterpret_cast<const float4*>(&s_e[j * CH + ch]);
-                const float4 B4 = *reinterpret_cast<const float4*>(&s_B[j * SP + s0]);
-                const float4 C4 = *reinterpret_cast<const float4*>(&s_C[j * SP + s0]);
-                const float B[4] = {B4.x, B4.y, B4.z, B4.w}, C[4] = {C4.x, C4.y, C4.z, C4.w};
-                float bc[8];
-                o[0][jj] = o[1][jj] = o[2][jj] = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a = ex2(e.x * A[i]);
-                    const float gg = fmaf(C[i], e.z, c[i]);
-                    const float ag = a * gg;
-                    const float w = ag * (j ? hs[j > 0 ? j - 1 : 0][i] : h[i]);
-                    bc[i] = gg * e.y;
-                    bc[4 + i] = hs[j][i] * e.z;
-                    o[0][jj] = fmaf(gg, B[i], o[0][jj]);
-                    o[1][jj] = fmaf(w, A[i], o[1][jj]);
-                    o[2][jj] = fmaf(hs[j][i], C[i], o[2][jj]);
-                    dA[i] = fmaf(w, e.x, dA[i]);
-                    c[i] = ag;
-                }
-                fold<8, NL, L>(bc, lane);
-                constexpr int KEEP = NL >= 8 ? 1 : 8 / NL;
-                constexpr int BITS = NL >= 8 ? 3 : (NL == 4 ? 2 : (NL == 2 ? 1 : 0));
-                if (lane / L < 8) {
-                    const int at = fold_index<BITS>(lane, L) * KEEP;  // of {B: 0..3, C: 4..7}
-#pragma unroll
-                    for (int i = 0; i < KEEP; ++i) {
-                        const int v = at + i;
-                        s_w[((warp * TT + j) * 2 + (v >> 2)) * SP + s0 + (v & 3)] = bc[i];
-                    }
-                }
-            }
-            constexpr int KEEP = L >= 4 ? 1 : 4 / L;
-            constexpr int BITS = L >= 4 ? 2 : (L == 2 ? 1 : 0);
-#pragma unroll
-            for (int w = 0; w < 3; ++w) {
-                fold<4, L, 1>(o[w], lane);
-                if (tid % L < 4) {
-                    const int at = jb + fold_index<BITS>(lane, 1) * KEEP;
-#pragma unroll
-                    for (int i = 0; i < KEEP; ++i) s_o[(w * TT + at + i) * YP + ch] = o[w][i];
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = next[i];
         __syncthreads();
         // gradients per (token, channel)
 #pragma unroll
@@ -413,19 +432,20 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
             const int tt = (tid + k2 * kThreads) / Q;
             if (tt >= TT || t + tt >= end || q4 >= nch) continue;
             float x[4], dl[4], zz[4], dout[4], gb4[4], sa[4], y[4], r[4];
-            u_now.r[k2].get(x);
-            d_now.r[k2].get(dl);
-            o_now.r[k2].get(dout);
+            feed.u.r[k2].get(x);
+            feed.d.r[k2].get(dl);
+            feed.o.r[k2].get(dout);
             load_vec<4>(&s_o[(0 * TT + tt) * YP + q4], gb4);
             load_vec<4>(&s_o[(1 * TT + tt) * YP + q4], sa);
-            load_vec<4>(&s_o[(2 * TT + tt) * YP + q4], y);
             const size_t at = (size_t)(t + tt) * D + c0 + q4;
             if (p.f.z) {
-                z_now.r[k2].get(zz);
+                feed.z.r[k2].get(zz);
+                load_vec<4>(&s_o[(2 * TT + tt) * YP + q4], y);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    r[i] = dout[i] * fmaf(skip[i], x[i], y[i]) * silu_slope(zz[i]);
-                    dout[i] *= silu(zz[i]);
+                    const float sg = sigmoid(zz[i]);
+                    r[i] = dout[i] * fmaf(skip[i], x[i], y[i]) * (sg * fmaf(zz[i], 1.f - sg, 1.f));
+                    dout[i] *= zz[i] * sg;
                 }
                 store4(p.gz + at, r, p.f.vec_d, nch - q4);
             }
@@ -444,6 +464,7 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
             }
             store4(p.gdelta + at, r, p.f.vec_d, nch - q4);
         }
+        if (k > 0) feed.fetch(p, t - TT, end, c0, nch, g, tid);
         // dB and dC of this block's channels
         for (int q = tid; q < TT * 2 * SP; q += kThreads) {
             const int j = q / (2 * SP), ws = q - j * 2 * SP, s = ws % SP;
@@ -457,11 +478,12 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
     }
 
     if (chan) {
+        const float dA[4] = {dA01.x, dA01.y, dA23.x, dA23.y}, c_in[4] = {c01.x, c01.y, c23.x, c23.y};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (s0 + i < S) {
                 p.part_A[(size_t)slot * DS + row + s0 + i] = dA[i];
-                if (seg == 0 && p.ginit) p.ginit[(size_t)n * DS + row + s0 + i] = c[i];
+                if (seg == 0 && p.ginit) p.ginit[(size_t)n * DS + row + s0 + i] = c_in[i];
             }
     }
     float* red = reinterpret_cast<float*>(smem);

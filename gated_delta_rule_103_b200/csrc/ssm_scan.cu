@@ -58,6 +58,9 @@ kda_ssm_scan_kernel(Params<T> p)
         }
     }
 
+    const float2 A01 = make_float2(A[0], A[1]), A23 = make_float2(A[2], A[3]);
+    float2 h01 = make_float2(h[0], h[1]), h23 = make_float2(h[2], h[3]);
+
     // this thread's channel quad when tiles are staged and written out
     const int q4 = (tid % Q) * 4;
     float bias[4], skip[4];
@@ -123,14 +126,13 @@ kda_ssm_scan_kernel(Params<T> p)
             for (int j = 0; j < 4; ++j) {
                 const float2 dd = s_dt[buf][tb + j][ch];
                 const float4 B = *reinterpret_cast<const float4*>(&s_B[buf][(tb + j) * SP + s0]);
-                const float a0 = ex2(dd.x * A[0]), a1 = ex2(dd.x * A[1]), a2 = ex2(dd.x * A[2]), a3 = ex2(dd.x * A[3]);
-                h[0] = fmaf(a0, h[0], dd.y * B.x);
-                h[1] = fmaf(a1, h[1], dd.y * B.y);
-                h[2] = fmaf(a2, h[2], dd.y * B.z);
-                h[3] = fmaf(a3, h[3], dd.y * B.w);
+                const float2 dt = both(dd.x), du = both(dd.y);
+                h01 = fma2(ex2(mul2(dt, A01)), h01, mul2(du, make_float2(B.x, B.y)));
+                h23 = fma2(ex2(mul2(dt, A23)), h23, mul2(du, make_float2(B.z, B.w)));
                 if constexpr (!kCarry) {
                     const float4 C = *reinterpret_cast<const float4*>(&s_C[buf][(tb + j) * SP + s0]);
-                    y[j] = fmaf(h[0], C.x, h[1] * C.y) + fmaf(h[2], C.z, h[3] * C.w);
+                    const float2 yy = fma2(h01, make_float2(C.x, C.y), mul2(h23, make_float2(C.z, C.w)));
+                    y[j] = yy.x + yy.y;
                 }
             }
             if constexpr (!kCarry) {
@@ -167,6 +169,10 @@ kda_ssm_scan_kernel(Params<T> p)
         }
     }
 
+    h[0] = h01.x;
+    h[1] = h01.y;
+    h[2] = h23.x;
+    h[3] = h23.y;
     if constexpr (kCarry) {
         float* e = p.ends + (size_t)slot * p.D * p.S + row + s0;
 #pragma unroll
@@ -231,77 +237,78 @@ kda_ssm_chain_kernel(const float* __restrict__ A, const float* __restrict__ init
 
 // One token for each of N sequences, the state read and written once in place
 // (memory-bound).  L lanes share a channel, each holding 4 neighbouring
-// states: whole rows of states go by in 16-byte accesses.
-template <typename T, int L, bool kVec>
+// states: whole rows of states go by in 16-byte accesses.  A thread takes its
+// channel of R sequences, whose states are in flight together and share A.
+template <typename T, int L, bool kVec, int R>
 __global__ void __launch_bounds__(256)
 kda_ssm_step_kernel(const T* __restrict__ u, const T* __restrict__ delta, const float* __restrict__ A,
                     const T* __restrict__ Bm, const T* __restrict__ Cm, const float* __restrict__ skip,
                     const T* __restrict__ z, const float* __restrict__ delta_bias, float* state,
-                    T* __restrict__ out, long long rows, int D, int S, int Dg, int G, int use_softplus)
+                    T* __restrict__ out, int N, int D, int S, int Dg, int G, int across, int use_softplus)
 {
-    const long long r = ((long long)blockIdx.x * 256 + threadIdx.x) / L;  // n D + d
+    const int at = (int)(blockIdx.x % across) * (256 / L) + threadIdx.x / L;
+    const int n0 = (int)(blockIdx.x / across) * R;
     const int l = threadIdx.x % L, s0 = l * 4;
-    const bool live = r < rows;
-    const long long rr = live ? r : 0;
-    const int n = (int)(rr / D), d = (int)(rr - (long long)n * D);
-    float h[4], a[4], B[4], C[4];
-    float* st = state + (size_t)rr * S + s0;
-    const float* Ap = A + (size_t)d * S + s0;
-    const size_t bc = ((size_t)n * G + d / Dg) * S + s0;
-    if constexpr (kVec) {
-        if (s0 < S) {
-            load_vec<4>(st, h);
-            load_vec<4>(Ap, a);
-            load_vec<4>(Bm + bc, B);
-            load_vec<4>(Cm + bc, C);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = a[i] = B[i] = C[i] = 0.f;
+    const bool live = at < D;
+    const int d = live ? at : 0;
+    const int g = d / Dg;
+    float h[R][4], a[4], B[R][4], C[R][4], x[R][1], dv[R][1], zz[R][1];
+    auto row4 = [&](const auto* p, float(&v)[4]) {
+        if constexpr (kVec) {
+            if (s0 < S) {
+                load_vec<4>(p, v);
+                return;
+            }
         }
-    } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const bool ok = s0 + i < S;
-            float v[1];
-            h[i] = ok ? st[i] : 0.f;
-            a[i] = ok ? Ap[i] : 0.f;
-            v[0] = 0.f;
-            if (ok) load_vec<1>(Bm + bc + i, v);
-            B[i] = v[0];
-            v[0] = 0.f;
-            if (ok) load_vec<1>(Cm + bc + i, v);
-            C[i] = v[0];
+            float w[1] = {0.f};
+            if (!kVec && s0 + i < S) load_vec<1>(p + i, w);
+            v[i] = w[0];
         }
-    }
-    float x[1], dv[1], zz[1] = {0.f};
-    load_vec<1>(u + rr, x);
-    load_vec<1>(delta + rr, dv);
-    if (z) load_vec<1>(z + rr, zz);
-    float dt = dv[0] + (delta_bias ? delta_bias[d] : 0.f);
-    if (use_softplus) dt = softplus(dt);
-    const float du = dt * x[0];
-    float y = 0.f;
+    };
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        h[i] = fmaf(ex2(dt * (a[i] * kLog2e)), h[i], du * B[i]);
-        y = fmaf(h[i], C[i], y);
+    for (int r = 0; r < R; ++r) {
+        const int n = n0 + r < N ? n0 + r : N - 1;
+        row4(state + ((size_t)n * D + d) * S + s0, h[r]);
     }
-    if (live) {
-        if constexpr (kVec) {
-            if (s0 < S) store_vec<4>(st, h);
-        } else {
+    row4(A + (size_t)d * S + s0, a);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (s0 + i < S) st[i] = h[i];
+    for (int r = 0; r < R; ++r) {
+        const int n = n0 + r < N ? n0 + r : N - 1;
+        const size_t bc = ((size_t)n * G + g) * S + s0, nd = (size_t)n * D + d;
+        row4(Bm + bc, B[r]);
+        row4(Cm + bc, C[r]);
+        load_vec<1>(u + nd, x[r]);
+        load_vec<1>(delta + nd, dv[r]);
+        zz[r][0] = 0.f;
+        if (z) load_vec<1>(z + nd, zz[r]);
+    }
+    const float bias = delta_bias ? delta_bias[d] : 0.f, sk = skip ? skip[d] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] *= kLog2e;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int n = n0 + r;
+        float dt = dv[r][0] + bias;
+        if (use_softplus) dt = softplus(dt);
+        const float du = dt * x[r][0];
+        float y = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[r][i] = fmaf(ex2(dt * a[i]), h[r][i], du * B[r][i]);
+            y = fmaf(h[r][i], C[r][i], y);
         }
-    }
+        const bool here = live && n < N;
+        if (here) store4(state + ((size_t)n * D + d) * S + s0, h[r], kVec && s0 < S, S - s0);
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (live && l == 0) {
-        y = fmaf(skip ? skip[d] : 0.f, x[0], y);
-        if (z) y *= silu(zz[0]);
-        const float o[1] = {y};
-        store_vec<1>(out + rr, o);
+        for (int o = L / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+        if (here && l == 0) {
+            y = fmaf(sk, x[r][0], y);
+            if (z) y *= silu(zz[r][0]);
+            const float o[1] = {y};
+            store_vec<1>(out + (size_t)n * D + d, o);
+        }
     }
 }
 
@@ -331,13 +338,18 @@ cudaError_t fwd(const ScanArgs& a, cudaStream_t st)
 template <typename T, int L>
 cudaError_t step(const ScanArgs& a, cudaStream_t st)
 {
-    const long long rows = (long long)a.N * a.D, blocks = (rows * L + 255) / 256;
+    const int across = (int)(((long long)a.D * L + 255) / 256);
+    // four sequences a thread once that still fills every SM's threads
+    const int R = (long long)across * a.N >= 4LL * 8 * sm_count() ? 4 : 1;
+    const long long blocks = (long long)across * ((a.N + R - 1) / R);
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (blocks == 0) return cudaSuccess;
-    auto* k = a.S % 4 == 0 ? &kda_ssm_step_kernel<T, L, true> : &kda_ssm_step_kernel<T, L, false>;
+    const bool vec = a.S % 4 == 0;
+    auto* k = R == 4 ? (vec ? &kda_ssm_step_kernel<T, L, true, 4> : &kda_ssm_step_kernel<T, L, false, 4>)
+                     : (vec ? &kda_ssm_step_kernel<T, L, true, 1> : &kda_ssm_step_kernel<T, L, false, 1>);
     k<<<(unsigned)blocks, 256, 0, st>>>((const T*)a.u, (const T*)a.delta, a.A, (const T*)a.Bm, (const T*)a.Cm, a.skip,
-                                        (const T*)a.z, a.delta_bias, a.final_state, (T*)a.out, rows, a.D, a.S,
-                                        a.D / a.G, a.G, a.softplus);
+                                        (const T*)a.z, a.delta_bias, a.final_state, (T*)a.out, a.N, a.D, a.S,
+                                        a.D / a.G, a.G, across, a.softplus);
     return cudaGetLastError();
 }
 

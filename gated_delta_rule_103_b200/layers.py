@@ -11,22 +11,24 @@ allocates belongs to that stream too.
 """
 from __future__ import annotations
 
-from contextlib import nullcontext
 from typing import Optional, Tuple
 
 import torch
 
 from .binding import (KDA_DTYPE_BF16, KDA_DTYPE_F32, KDA_FLAG_PER_TOKEN, KDA_FLAG_SILU,
-                      KDA_FLAG_SOFTPLUS, _check, load_library)
+                      KDA_FLAG_SOFTPLUS, KDAError, load_library)
 
-_F32 = torch.float32
+_F32, _BF16 = torch.float32, torch.bfloat16
 _ACTIVATIONS = {None: 0, "silu": KDA_FLAG_SILU}
 
 
+# A one-token call takes about as long to check and marshal as to run, so what
+# follows does one plain attribute test after the other.
+
 def _dtype(t: torch.Tensor, name: str) -> int:
-    if t.dtype == torch.bfloat16:
+    if t.dtype is _BF16:
         return KDA_DTYPE_BF16
-    if t.dtype == _F32:
+    if t.dtype is _F32:
         return KDA_DTYPE_F32
     raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
 
@@ -37,7 +39,7 @@ def _take(t: Optional[torch.Tensor], name: str, shape, dtype) -> Optional[int]:
         return None
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device (no CPU fallback)")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -70,13 +72,32 @@ def _rank(t: torch.Tensor, name: str, n: int):
     return t.shape
 
 
-def _on(stream):
+class _On:
     """What a call allocates, it allocates for the stream that it runs on."""
-    return nullcontext() if stream is None else torch.cuda.stream(stream)
+
+    __slots__ = ("context",)
+
+    def __init__(self, stream):
+        self.context = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.context is not None:
+            self.context.__enter__()
+
+    def __exit__(self, *error):
+        if self.context is not None:
+            self.context.__exit__(*error)
 
 
-def _raw(stream) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _raw(stream, t: torch.Tensor) -> int:
+    """The stream's handle: the given one, or the current one of t's device
+    (the library refuses tensors of another device than the current one)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+
+
+def _check(status: int, where: str):
+    if status:
+        raise KDAError(status, where)
 
 
 def _space(need: int, workspace: Optional[torch.Tensor], device):
@@ -117,14 +138,14 @@ def short_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     state = (N, W - 1, C)
     px, pw = _take(x, "x", x.shape, dtype), _take(weight, "weight", (C, W), _F32)
     pb, ps = _take(bias, "bias", (C,), _F32), _take(initial_state, "initial_state", state, dtype)
-    with _on(stream):
+    with _On(stream):
         if out is None:
             out = torch.empty_like(x)
         if final_state is None and output_final_state:
             final_state = torch.empty(state, dtype=dtype, device=x.device)
         _check(lib.kda_short_conv_fwd(px, pw, pb, ps, cu, _take(out, "out", x.shape, dtype),
                                       _take(final_state, "final_state", state, dtype),
-                                      B, T, C, W, N, dt, flags, _raw(stream)), "kda_short_conv_fwd")
+                                      B, T, C, W, N, dt, flags, _raw(stream, x)), "kda_short_conv_fwd")
     return out, final_state
 
 
@@ -141,11 +162,14 @@ def short_conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor,
     flags = _activation(activation)
     px, pw = _take(x, "x", x.shape, dtype), _take(weight, "weight", (C, W), _F32)
     pb, ps = _take(bias, "bias", (C,), _F32), _take(state, "state", (N, W - 1, C), dtype)
-    with _on(stream):
-        if out is None:
+    if out is None:
+        if stream is None:
             out = torch.empty_like(x)
-        _check(lib.kda_short_conv_step(px, pw, pb, ps, _take(out, "out", x.shape, dtype), N, C, W, dt,
-                                       flags, _raw(stream)), "kda_short_conv_step")
+        else:
+            with _On(stream):
+                out = torch.empty_like(x)
+    _check(lib.kda_short_conv_step(px, pw, pb, ps, _take(out, "out", x.shape, dtype), N, C, W, dt,
+                                   flags, _raw(stream, x)), "kda_short_conv_step")
     return out
 
 
@@ -182,7 +206,7 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, d_out: torch.Tensor,
            _take(bias, "bias", (C,), _F32), _take(initial_state, "initial_state", state, dtype), cu,
            _take(d_out, "d_out", x.shape, dtype), _take(d_final_state, "d_final_state", state, _F32))
     shapes = ((B, T, C), (C, W), (C,), state)
-    with _on(stream):
+    with _On(stream):
         if grads is None:
             wanted = (True, True, bias is not None, need_initial_state_grad)
             grads = [torch.empty(s, dtype=_F32, device=x.device) if w else None
@@ -194,7 +218,7 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, d_out: torch.Tensor,
         ws, size, _keep = _space(
             int(lib.kda_short_conv_bwd_workspace_bytes(B, T, C, W, N, cu is not None, dt)), workspace,
             x.device)
-        _check(lib.kda_short_conv_bwd(*ins, *outs, B, T, C, W, N, dt, flags, ws, size, _raw(stream)),
+        _check(lib.kda_short_conv_bwd(*ins, *outs, B, T, C, W, N, dt, flags, ws, size, _raw(stream, x)),
                "kda_short_conv_bwd")
     return dx, dw, db, ds
 
@@ -257,7 +281,7 @@ def ssm_scan_fwd(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch
     flags = KDA_FLAG_SOFTPLUS if softplus else 0
     state = (N, ch, S)
     ps = _take(initial_state, "initial_state", state, _F32)
-    with _on(stream):
+    with _On(stream):
         if out is None:
             out = torch.empty_like(u)
         if final_state is None and output_final_state:
@@ -267,7 +291,7 @@ def ssm_scan_fwd(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch
             u.device)
         _check(lib.kda_ssm_scan_fwd(*ins, ps, cu, _take(out, "out", u.shape, u.dtype),
                                     _take(final_state, "final_state", state, _F32), b, T, ch, S, G, N,
-                                    dt, flags, ws, size, _raw(stream)), "kda_ssm_scan_fwd")
+                                    dt, flags, ws, size, _raw(stream, u)), "kda_ssm_scan_fwd")
     return out, final_state
 
 
@@ -283,11 +307,14 @@ def ssm_step(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch.Ten
     ins, ch, S, G = _scan_inputs(u, delta, A, B, C, D, z, delta_bias, 1)
     N = u.shape[0]
     ps = _take(state, "state", (N, ch, S), _F32)
-    with _on(stream):
-        if out is None:
+    if out is None:
+        if stream is None:
             out = torch.empty_like(u)
-        _check(lib.kda_ssm_step(*ins, ps, _take(out, "out", u.shape, u.dtype), N, ch, S, G, dt,
-                                KDA_FLAG_SOFTPLUS if softplus else 0, _raw(stream)), "kda_ssm_step")
+        else:
+            with _On(stream):
+                out = torch.empty_like(u)
+    _check(lib.kda_ssm_step(*ins, ps, _take(out, "out", u.shape, u.dtype), N, ch, S, G, dt,
+                            KDA_FLAG_SOFTPLUS if softplus else 0, _raw(stream, u)), "kda_ssm_step")
     return out
 
 
@@ -315,7 +342,7 @@ def ssm_scan_bwd(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch
     ins += (_take(initial_state, "initial_state", state, _F32), cu, _take(d_out, "d_out", u.shape, u.dtype),
             _take(d_final_state, "d_final_state", state, _F32))
     shapes = (u.shape, u.shape, A.shape, B.shape, B.shape, (ch,), u.shape, (ch,), state)
-    with _on(stream):
+    with _On(stream):
         if grads is None:
             wanted = (True, True, True, True, True, D is not None, z is not None, delta_bias is not None,
                       need_initial_state_grad)
@@ -329,7 +356,7 @@ def ssm_scan_bwd(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch
             int(lib.kda_ssm_scan_bwd_workspace_bytes(b, T, ch, S, G, N, cu is not None, dt)), workspace,
             u.device)
         _check(lib.kda_ssm_scan_bwd(*ins, *outs, b, T, ch, S, G, N, dt, KDA_FLAG_SOFTPLUS if softplus else 0,
-                                    ws, size, _raw(stream)), "kda_ssm_scan_bwd")
+                                    ws, size, _raw(stream, u)), "kda_ssm_scan_bwd")
     return du, dd, dA, dB, dC, dD, dz, dbias, ds
 
 
@@ -373,7 +400,7 @@ def group_norm_fwd(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] 
     lib = load_library()
     dt = _dtype(x, "x")
     ins, B, T, C, N, flags, stat = _norm_inputs(x, groups, weight, bias, activation, per_token, cu_seqlens)
-    with _on(stream):
+    with _On(stream):
         if out is None:
             out = torch.empty_like(x)
         if mean is None:
@@ -385,7 +412,7 @@ def group_norm_fwd(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] 
         ws, size, _keep = _space(need, workspace, x.device)
         _check(lib.kda_group_norm_fwd(*ins, eps, _take(out, "out", x.shape, x.dtype),
                                       _take(mean, "mean", stat, _F32), _take(rstd, "rstd", stat, _F32),
-                                      B, T, C, groups, N, dt, flags, ws, size, _raw(stream)),
+                                      B, T, C, groups, N, dt, flags, ws, size, _raw(stream, x)),
                "kda_group_norm_fwd")
     return out, mean, rstd
 
@@ -407,7 +434,7 @@ def group_norm_bwd(x: torch.Tensor, groups: int, d_out: torch.Tensor, mean: torc
     ins += (_take(mean, "mean", stat, _F32), _take(rstd, "rstd", stat, _F32),
             _take(d_out, "d_out", x.shape, x.dtype))
     shapes = (x.shape, (C,), (C,))
-    with _on(stream):
+    with _On(stream):
         if grads is None:
             grads = [torch.empty(s, dtype=_F32, device=x.device) if w else None
                      for s, w in zip(shapes, (True, weight is not None, bias is not None))]
@@ -418,6 +445,6 @@ def group_norm_bwd(x: torch.Tensor, groups: int, d_out: torch.Tensor, mean: torc
         ws, size, _keep = _space(
             int(lib.kda_group_norm_bwd_workspace_bytes(B, T, C, groups, N, cu_seqlens is not None, dt, flags)),
             workspace, x.device)
-        _check(lib.kda_group_norm_bwd(*ins, *outs, B, T, C, groups, N, dt, flags, ws, size, _raw(stream)),
+        _check(lib.kda_group_norm_bwd(*ins, *outs, B, T, C, groups, N, dt, flags, ws, size, _raw(stream, x)),
                "kda_group_norm_bwd")
     return dx, dw, db
