@@ -97,10 +97,25 @@ struct Raw {
     __device__ __forceinline__ void get(float (&x)[V]) const { load_vec<V>(v, x); }
 };
 
-// 1 / (1 + e^-x) with the fast exponential and reciprocal (relative error of
-// some 2^-22: below the rounding of the products it enters).  e^-x = inf
-// gives 0.
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// 2^x, e^x and 1 / x in one or two instructions each, subnormals taken as zero
+// (relative errors of some 2^-22; handling subnormals would cost three times
+// the instructions).
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float fast_exp(float x) { return ex2(x * 1.4426950408889634f); }
+__device__ __forceinline__ float fast_rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 1 / (1 + e^-x).  e^-x = inf gives 0.
+__device__ __forceinline__ float sigmoid(float x) { return fast_rcp(1.f + fast_exp(-x)); }
 __device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
 // d silu(v) / dv = s (1 + v (1 - s)), s = sigmoid(v)
 __device__ __forceinline__ float silu_slope(float v)

@@ -24,8 +24,10 @@ namespace {
 
 using namespace ssm;
 
+constexpr int kThreads = 256;
+
 template <int L>
-using BTile = Tile<L, (L == 4 || L == 8) ? 16 : 8>;
+using BTile = Tile<L, 4, (L == 4 || L == 8) ? 16 : 8, kThreads>;
 
 template <typename T>
 struct BwdParams {
@@ -53,11 +55,14 @@ struct Feed {
     __device__ __forceinline__ void fetch(const BwdParams<T>& p, long long t, long long end, int c0, int nch, int g,
                                           int tid)
     {
-        u.load(p.f.u, p.f, t, end, c0, nch, tid);
-        d.load(p.f.delta, p.f, t, end, c0, nch, tid);
+        const int q4 = (tid % Tl::Q) * 4, nq = nch - q4, D = p.f.D;
+        const size_t at = (size_t)(t + tid / Tl::Q) * D + c0 + q4;
+        const int left = (end - t < Tl::TT ? (int)(end - t) : Tl::TT) - tid / Tl::Q;
+        u.load(p.f.u, at, D, left, nq, p.f.vec_d, tid);
+        d.load(p.f.delta, at, D, left, nq, p.f.vec_d, tid);
         if (kY) {
-            if (p.f.z) z.load(p.f.z, p.f, t, end, c0, nch, tid);
-            o.load(p.d_out, p.f, t, end, c0, nch, tid);
+            if (p.f.z) z.load(p.f.z, at, D, left, nq, p.f.vec_d, tid);
+            o.load(p.d_out, at, D, left, nq, p.f.vec_d, tid);
         }
         bc.load(p.f, t, end, g, tid);
     }
@@ -218,7 +223,7 @@ constexpr size_t bwd_smem()
     using Tl = BTile<L>;
     // staged operands, results per (token, channel), warps' sums of dB and dC,
     // entry states of every four tokens
-    return sizeof(float) * (2 * Tl::TT * Tl::CH * 4 + 4 * Tl::TT * Tl::SP + 3 * Tl::TT * Tl::YP +
+    return sizeof(float) * (2 * Tl::TT * Tl::CH * 4 + 4 * Tl::TT * Tl::SP + 3 * Tl::TT * (Tl::CH + 8) +
                             (kThreads / 32) * Tl::TT * 2 * Tl::SP + Tl::TT * kThreads);
 }
 
@@ -227,7 +232,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 kda_ssm_bwd_kernel(BwdParams<T> p)
 {
     using Tl = BTile<L>;
-    constexpr int CH = Tl::CH, TT = Tl::TT, SP = Tl::SP, Q = Tl::Q, YP = Tl::YP, IPT = Tl::IPT;
+    constexpr int CH = Tl::CH, TT = Tl::TT, SP = Tl::SP, Q = Tl::Q, IPT = Tl::IPT;
+    constexpr int YP = CH + 8;  // no two of a warp's results in one bank
     constexpr int WARPS = kThreads / 32, NL = 32 / L;               // channels of a warp
     extern __shared__ __align__(16) unsigned char smem[];
     Elem* s_e = reinterpret_cast<Elem*>(smem);                      // [2][TT][CH]
@@ -558,21 +564,28 @@ kda_ssm_bwd_params_kernel(const float* __restrict__ part_A, const float* __restr
 }
 
 // Another walk over the unit's tokens is a fifth of the whole.
-constexpr int kBwdWarps = 12, kBwdShortest = 64;
+constexpr int kBwdFewWarps = 12, kBwdWantWarps = 12, kBwdShortest = 64;
 
 struct Layout {
     Cut c;
     size_t slots, tiles, ends, exits, steps, entries, bc, A, d, total;
 };
 
+// Lanes that share a channel.
+int bwd_lanes(int S)
+{
+    int l = 1;
+    while (4 * l < S) l <<= 1;
+    return l;
+}
 int bwd_tile_tokens(int L) { return L == 4 || L == 8 ? 16 : 8; }
 
 Layout layout_of(int B, int T, int D, int S, int G, int N, int packed)
 {
     Layout l = {};
-    l.c = cut_of(B, T, D, S, N, packed, kBwdWarps, kBwdShortest);
+    const size_t tokens = (size_t)B * T, DS = (size_t)D * S, L = bwd_lanes(S);
+    l.c = cut_of(B, T, N, packed, (double)D * L / 32.0, kBwdFewWarps, kBwdWantWarps, kBwdShortest);
     l.slots = (size_t)slots_of(B, T, N, packed, l.c.len);
-    const size_t tokens = (size_t)B * T, DS = (size_t)D * S, L = lanes_of(S);
     const size_t CH = kThreads / L, cpb = ((size_t)(D / G) + CH - 1) / CH;
     l.tiles = tokens / bwd_tile_tokens((int)L) + l.slots + 1;
     size_t at = 0;
@@ -652,7 +665,7 @@ cudaError_t bwd(const ScanArgs& a, cudaStream_t st)
 template <typename T>
 cudaError_t by_states(const ScanArgs& a, cudaStream_t st)
 {
-    switch (lanes_of(a.S)) {
+    switch (bwd_lanes(a.S)) {
         case 1: return bwd<T, 1>(a, st);
         case 2: return bwd<T, 2>(a, st);
         case 4: return bwd<T, 4>(a, st);

@@ -4,11 +4,11 @@
 //     h[d, s] = a h[d, s] + dt u B[g, s];     y = sum_s h C[g, s] + skip u
 //     out = y, or y silu(z)
 //
-// Thread layout of every pass over tokens: a block of 256 threads takes 256 /
-// L channels of one group; L neighbouring lanes share a channel and hold 4
-// states each (S <= 4 L; states behind S have A = B = C = 0).  Tokens go by in
-// tiles: what depends on (token, channel) alone is computed once per element
-// and handed to the L lanes through shared memory.
+// Thread layout of every pass over tokens: a block takes THREADS / L channels
+// of one group; L neighbouring lanes share a channel and hold K states each (S
+// <= K L; states behind S have A = B = C = 0).  Tokens go by in tiles: what
+// depends on (token, channel) alone is computed once per element and handed to
+// the L lanes through shared memory.
 #pragma once
 
 #include "layer.h"
@@ -19,27 +19,21 @@ namespace ssm {
 
 using namespace layer;
 
-constexpr int kThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int L, int TOKENS = (L == 1 ? 4 : L == 2 ? 8 : 16)>
+template <int LANES, int STATES, int TOKENS, int BLOCK>
 struct Tile {
-    static constexpr int CH = kThreads / L;            // channels per block
+    static constexpr int L = LANES, K = STATES;
     static constexpr int TT = TOKENS;                  // tokens per tile
-    static constexpr int SP = 4 * L;                   // padded states
+    static constexpr int THREADS = BLOCK;
+    static constexpr int CH = THREADS / L;             // channels per block
+    static constexpr int SP = K * L;                   // padded states
     static constexpr int Q = CH / 4;                   // channel quads
-    static constexpr int IPT = (TT * Q + kThreads - 1) / kThreads;     // quads per thread
-    static constexpr int ROWS = kThreads / Q < TT ? kThreads / Q : TT;  // threads that share a quad
-    static constexpr int YP = CH + 8;                  // padded row of per-(token, channel) results
+    static constexpr int IPT = (TT * Q + THREADS - 1) / THREADS;      // quads per thread
+    static constexpr int ROWS = THREADS / Q < TT ? THREADS / Q : TT;  // threads that share a quad
+    static_assert(CH % 4 == 0 && (THREADS % Q == 0) && TT % 4 == 0, "tile");
 };
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // Two fp32 values in one instruction: half the issue slots of the products and
 // sums that surround the exponentials.
@@ -62,7 +56,8 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
     return d;
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-__device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
+using layer::ex2;
+__device__ __forceinline__ float2 ex2(float2 x) { return make_float2(layer::ex2(x.x), layer::ex2(x.y)); }
 
 // log(1 + e^x) = max(x, 0) + log1p(w), w = e^-|x|.  log1p(w) = 2 artanh(r)
 // with r = w / (2 + w) <= 1/3, by its power series to r^15 (the rest is below
@@ -70,8 +65,8 @@ __device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ex2(x.x), e
 // would lose.
 __device__ __forceinline__ float softplus(float x)
 {
-    const float w = __expf(-fabsf(x));
-    const float r = __fdividef(w, 2.f + w), q = r * r;
+    const float w = fast_exp(-fabsf(x));
+    const float r = w * fast_rcp(2.f + w), q = r * r;
     float p = 1.f / 15.f;
     p = fmaf(p, q, 1.f / 13.f);
     p = fmaf(p, q, 1.f / 11.f);
@@ -81,6 +76,22 @@ __device__ __forceinline__ float softplus(float x)
     p = fmaf(p, q, 1.f / 3.f);
     p = fmaf(p, q, 1.f);
     return fmaf(2.f * r, p, fmaxf(x, 0.f));
+}
+
+// ... of two values, the series in packed arithmetic.
+__device__ __forceinline__ float2 softplus2(float2 x)
+{
+    const float2 w = make_float2(fast_exp(-fabsf(x.x)), fast_exp(-fabsf(x.y)));
+    const float2 r = mul2(w, make_float2(fast_rcp(2.f + w.x), fast_rcp(2.f + w.y))), q = mul2(r, r);
+    float2 p = both(1.f / 15.f);
+    p = fma2(p, q, both(1.f / 13.f));
+    p = fma2(p, q, both(1.f / 11.f));
+    p = fma2(p, q, both(1.f / 9.f));
+    p = fma2(p, q, both(1.f / 7.f));
+    p = fma2(p, q, both(1.f / 5.f));
+    p = fma2(p, q, both(1.f / 3.f));
+    p = fma2(p, q, both(1.f));
+    return fma2(mul2(r, both(2.f)), p, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
 }
 
 // Four values as they lie in memory, loaded before they are needed.
@@ -191,22 +202,40 @@ __device__ __forceinline__ int fold_index(int lane, int stride)
 // [token][SP] in shared memory.
 template <typename T, typename Tl, bool kC>
 struct StateRows {
-    static constexpr int TT = Tl::TT, L = Tl::SP / 4, ALL = (kC ? 2 : 1) * TT * L;
-    static constexpr int NB = (ALL + kThreads - 1) / kThreads;
+    static constexpr int TT = Tl::TT, SQ = Tl::SP / 4, ONE = TT * SQ, ALL = (kC ? 2 : 1) * ONE;
+    static constexpr int NB = (ALL + Tl::THREADS - 1) / Tl::THREADS;
+    // whole rounds of the threads over B, then C: which is which is known at compile time
+    static constexpr bool kRounds = ONE % Tl::THREADS == 0 && Tl::THREADS % SQ == 0;
     Raw4<T> r[NB];
     __device__ __forceinline__ void load(const Params<T>& p, long long t0, long long end, int g, int tid)
     {
+        const int left = end - t0 < TT ? (int)(end - t0) : TT;
+        const int s = (tid % SQ) * 4;
+        if constexpr (kRounds) {
+            constexpr int PER = ONE / Tl::THREADS, STEP = Tl::THREADS / SQ;
+            const size_t at = ((size_t)(t0 + tid / SQ) * p.G + g) * p.S + s;
+            const size_t step = (size_t)STEP * p.G * p.S;
 #pragma unroll
-        for (int k = 0; k < NB; ++k) {
-            const int i = tid + k * kThreads;
-            const int which = i / (TT * L), j = i - which * (TT * L);
-            const long long t = t0 + j / L;
-            const int s = (j % L) * 4;
-            r[k].zero();
-            if (i < ALL && t < end && s < p.S) {
-                const T* q = (kC && which ? p.Cm : p.Bm) + ((size_t)t * p.G + g) * p.S + s;
-                if (p.vec_s) r[k].load(q);
-                else r[k].load_some(q, p.S - s);
+            for (int k = 0; k < NB; ++k) {
+                const int j = k % PER;
+                r[k].zero();
+                if (tid / SQ + j * STEP < left && s < p.S) {
+                    const T* q = (k < PER ? p.Bm : p.Cm) + at + j * step;
+                    if (p.vec_s) r[k].load(q);
+                    else r[k].load_some(q, p.S - s);
+                }
+            }
+        } else {
+            static_assert(Tl::THREADS % SQ == 0, "state quads");
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                const int i = tid + k * Tl::THREADS, t = i % ONE / SQ;
+                r[k].zero();
+                if (i < ALL && t < left && s < p.S) {
+                    const T* q = (kC && i >= ONE ? p.Cm : p.Bm) + ((size_t)(t0 + t) * p.G + g) * p.S + s;
+                    if (p.vec_s) r[k].load(q);
+                    else r[k].load_some(q, p.S - s);
+                }
             }
         }
     }
@@ -214,44 +243,43 @@ struct StateRows {
     {
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            const int i = tid + k * kThreads;
-            const int which = i / (TT * L), j = i - which * (TT * L);
-            if (i < ALL) {
-                float x[4];
-                r[k].get(x);
-                *reinterpret_cast<float4*>((kC && which ? sC : sB) + j * 4) = make_float4(x[0], x[1], x[2], x[3]);
+            const int i = tid + k * Tl::THREADS;
+            float* to;
+            if constexpr (kRounds) {
+                constexpr int PER = ONE / Tl::THREADS;
+                to = (k < PER ? sB : sC) + (tid + k % PER * Tl::THREADS) * 4;
+            } else {
+                if (i >= ALL) break;
+                to = (kC && i >= ONE ? sC : sB) + i % ONE * 4;
             }
+            float x[4];
+            r[k].get(x);
+            *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
         }
     }
 };
 
-// Rows of one (token, channel) operand of one tile, raw.
+// Rows of one (token, channel) operand of one tile, raw.  Thread tid takes the
+// channel quad tid % Q of tokens tid / Q, tid / Q + THREADS / Q, ...: `at` is
+// its first element's offset, `left` the tokens from there to the unit's end.
 template <typename T, typename Tl>
 struct ChannelRows {
+    static constexpr int STEP = Tl::THREADS / Tl::Q;
     Raw4<T> r[Tl::IPT];
-    __device__ __forceinline__ void load(const T* base, const Params<T>& p, long long t0, long long end, int c0,
-                                         int nch, int tid)
+    __device__ __forceinline__ void load(const T* base, size_t at, int D, int left, int n, bool vec, int tid)
     {
 #pragma unroll
         for (int k = 0; k < Tl::IPT; ++k) {
-            const int i = tid + k * kThreads;
-            const int t = i / Tl::Q, c = (i % Tl::Q) * 4;
             r[k].zero();
-            if (t < Tl::TT && t0 + t < end && c < nch) {
-                const T* q = base + (size_t)(t0 + t) * p.D + c0 + c;
-                if (p.vec_d) r[k].load(q);
-                else r[k].load_some(q, nch - c);
+            const bool in_tile = Tl::Q * Tl::TT >= Tl::THREADS || tid / Tl::Q < Tl::TT;
+            if (in_tile && k * STEP < left && n > 0) {
+                const T* q = base + at + (size_t)(k * STEP) * D;
+                if (vec) r[k].load(q);
+                else r[k].load_some(q, n);
             }
         }
     }
 };
-
-inline int lanes_of(int S)
-{
-    int l = 1;
-    while (4 * l < S) l <<= 1;
-    return l;
-}
 
 inline Units units_of(const int32_t* cu, int B, int T, int N, int len)
 {
@@ -277,22 +305,23 @@ struct Cut {
     int len;
     bool cut;
 };
-// Cut only where the chains' warps (L lanes a channel) leave the SMs under
-// `warps` warps each; no unit is shorter than `shortest` tokens.
-inline Cut cut_of(int B, int T, int D, int S, int N, int packed, int warps, int shortest)
+// Cut only where the chains (chain_warps warps a sequence) give the SMs under
+// `few` warps each, then into units that give them `want`; no unit is shorter
+// than `shortest` tokens.
+inline Cut cut_of(int B, int T, int N, int packed, double chain_warps, int few, int want, int shortest)
 {
     Cut c = {T > 0 ? (T + 15) / 16 * 16 : 16, false};
     const long long tokens = (long long)B * T;
     if (tokens == 0 || N == 0) return c;
-    const double chain_warps = (double)D * lanes_of(S) / 32.0;  // of one sequence
-    const double units = (double)sm_count() * warps / chain_warps;
+    const bool many = (double)sm_count() * few <= chain_warps * N;
+    if (many && !packed) return c;
+    const double units = (double)sm_count() * want / chain_warps;
     double len = (double)tokens / (units < 1.0 ? 1.0 : units);
     if (packed) {
-        // the longest sequence is not known here: no unit is longer than twice the mean
+        // the longest sequence is not known here: no unit is longer than twice
+        // the mean, and where there are many chains none shorter
         const double mean = 2.0 * (double)tokens / N;
-        if (len > mean) len = mean;
-    } else if (len >= T) {
-        return c;
+        if (many || len > mean) len = mean;
     }
     long long l = ((long long)len + 15) / 16 * 16;
     if (l < shortest) l = shortest;

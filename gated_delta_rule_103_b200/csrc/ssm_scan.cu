@@ -16,20 +16,39 @@ namespace {
 
 using namespace ssm;
 
+// A block is one warp and needs no barrier.  L lanes share two channels and
+// hold four states of each: what a lane reads of B and C from shared memory
+// then serves eight states (each 16-byte read returns 512 bytes to a warp's
+// registers, four clocks of an SM's 128 bytes; one channel a lane would spend as
+// long on them as on the exponentials).  What depends on (token, channel) alone
+// is worked out once, by the lane that also ends up with its output: in a batch
+// of TB = L / 2 tokens, lane l has channel l % 2 and one token, and the fold
+// over the lanes of the batch's 2 TB outputs leaves each with its own.
+template <int LANES>
+struct Fwd {
+    static constexpr int L = LANES, THREADS = 32;
+    static constexpr int PAIRS = 32 / L, CH = 2 * PAIRS, SP = 4 * L;
+    static constexpr int TB = L >= 2 ? L / 2 : 1;          // tokens per batch
+    static constexpr int TT = L >= 4 ? 16 : 4 * L;         // tokens per tile
+    static constexpr int NB = TT / TB;                     // batches per tile
+    static constexpr int OWN = L == 1 ? 2 : 1;             // elements of a lane per batch
+    static constexpr int BITS = L == 32 ? 4 : L == 16 ? 3 : L == 8 ? 2 : L == 4 ? 1 : 0;  // log2 TB
+};
+
 // kCarry: the first pass, end state from zero and sum of dt of every unit that
 // another one follows.
-template <typename T, int L, bool kCarry>
-__global__ void __launch_bounds__(kThreads, 2)
+template <typename T, int LANES, bool kCarry>
+__global__ void __launch_bounds__(32, 10)
 kda_ssm_scan_kernel(Params<T> p)
 {
-    using Tl = Tile<L>;
-    constexpr int CH = Tl::CH, TT = Tl::TT, SP = Tl::SP, Q = Tl::Q, YP = Tl::YP, IPT = Tl::IPT;
-    __shared__ __align__(16) float2 s_dt[2][TT][CH];  // dt, dt u
-    __shared__ __align__(16) float s_B[2][TT * SP];
-    __shared__ __align__(16) float s_C[kCarry ? 1 : 2][kCarry ? 4 : TT * SP];
-    __shared__ __align__(16) float s_y[kCarry ? 1 : 2][kCarry ? 4 : TT * YP];
+    using Tl = Fwd<LANES>;
+    constexpr int L = Tl::L, CH = Tl::CH, TT = Tl::TT, SP = Tl::SP, TB = Tl::TB, NB = Tl::NB, OWN = Tl::OWN;
+    constexpr int PAIRS = Tl::PAIRS;
+    __shared__ __align__(16) float2 s_dt[TT][PAIRS][2];  // dt, dt u
+    __shared__ __align__(16) float s_B[TT * SP];
+    __shared__ __align__(16) float s_C[kCarry ? 4 : TT * SP];
 
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int lane = threadIdx.x & 31;
     const int across = p.G * p.cpb;
     const long long slot = blockIdx.x / across;
     const int gb = (int)(blockIdx.x % across), g = gb / p.cpb;
@@ -42,160 +61,188 @@ kda_ssm_scan_kernel(Params<T> p)
     const int nch = p.Dg - cg < CH ? p.Dg - cg : CH;       // channels of this block
     const int c0 = g * p.Dg + cg;
 
-    // this thread's channel and states
-    const int ch = tid / L, s0 = (tid % L) * 4;
-    const bool chan = ch < nch;
-    const size_t row = (size_t)(c0 + (chan ? ch : 0)) * p.S;
-    float A[4], h[4];
+    // this lane's states of its pair's channels (a channel behind the last stands
+    // for the last and is not stored)
+    const int pair = lane / L, s0 = (lane % L) * 4;
+    float A[2][4], h[2][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool ok = chan && s0 + i < p.S;
-        A[i] = ok ? p.A[row + s0 + i] * kLog2e : 0.f;
-        h[i] = 0.f;
-        if (ok && !kCarry) {
-            if (p.ends) h[i] = p.ends[(size_t)slot * p.D * p.S + row + s0 + i];
-            else if (p.init) h[i] = p.init[(size_t)n * p.D * p.S + row + s0 + i];
-        }
-    }
-
-    const float2 A01 = make_float2(A[0], A[1]), A23 = make_float2(A[2], A[3]);
-    float2 h01 = make_float2(h[0], h[1]), h23 = make_float2(h[2], h[3]);
-
-    // this thread's channel quad when tiles are staged and written out
-    const int q4 = (tid % Q) * 4;
-    float bias[4], skip[4];
+    for (int r = 0; r < 2; ++r) {
+        const int c = pair * 2 + r;
+        const size_t row = (size_t)(c0 + (c < nch ? c : nch - 1)) * p.S + s0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        bias[i] = p.delta_bias && q4 + i < nch ? p.delta_bias[c0 + q4 + i] : 0.f;
-        skip[i] = p.skip && q4 + i < nch ? p.skip[c0 + q4 + i] : 0.f;
-    }
-
-    ChannelRows<T, Tl> u, d, z, u_now, z_now;
-    StateRows<T, Tl, !kCarry> bc;
-    float dt_sum[4] = {0.f, 0.f, 0.f, 0.f};
-
-    auto fetch = [&](long long t) {
-        u.load(p.u, p, t, end, c0, nch, tid);
-        d.load(p.delta, p, t, end, c0, nch, tid);
-        if (!kCarry && p.z) z.load(p.z, p, t, end, c0, nch, tid);
-        bc.load(p, t, end, g, tid);
-    };
-    auto stage = [&](long long t, int buf) {
-#pragma unroll
-        for (int k = 0; k < IPT; ++k) {
-            const int tt = (tid + k * kThreads) / Q;
-            if (tt >= TT) break;
-            float x[4], dv[4];
-            u.r[k].get(x);
-            d.r[k].get(dv);
-            const bool in = t + tt < end;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float v = dv[i] + bias[i];
-                if (p.softplus) v = softplus(v);
-                if (!in) v = 0.f;
-                if (kCarry) dt_sum[i] += v;
-                dv[i] = v;
+        for (int i = 0; i < 4; ++i) {
+            const bool ok = s0 + i < p.S;
+            A[r][i] = ok ? p.A[row + i] * kLog2e : 0.f;
+            h[r][i] = 0.f;
+            if (ok && !kCarry) {
+                if (p.ends) h[r][i] = p.ends[(size_t)slot * p.D * p.S + row + i];
+                else if (p.init) h[r][i] = p.init[(size_t)n * p.D * p.S + row + i];
             }
-            float4* o = reinterpret_cast<float4*>(&s_dt[buf][tt][q4]);
-            o[0] = make_float4(dv[0], dv[0] * x[0], dv[1], dv[1] * x[1]);
-            o[1] = make_float4(dv[2], dv[2] * x[2], dv[3], dv[3] * x[3]);
         }
-        bc.put(s_B[buf], s_C[kCarry ? 0 : buf], tid);
+    }
+
+    // this lane's own elements: tokens TB e + tok of the channels own[], e = 0 .. NB - 1
+    const int tok = fold_index<Tl::BITS>(lane, 2);
+    int own[OWN];
+    float bias[OWN], skip[OWN], dt_sum[OWN];
+    bool mine[OWN];
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+        const int c = pair * 2 + (OWN == 2 ? o : lane & 1);
+        mine[o] = c < nch;
+        own[o] = c0 + (c < nch ? c : nch - 1);
+        bias[o] = p.delta_bias ? p.delta_bias[own[o]] : 0.f;
+        skip[o] = p.skip ? p.skip[own[o]] : 0.f;
+        dt_sum[o] = 0.f;
+    }
+    const bool gate = !kCarry && p.z;
+
+    T u[NB][OWN], d[NB][OWN], z[NB][OWN];
+    StateRows<T, Tl, !kCarry> bc;
+    // the tile from token t on (tokens behind the end repeat the last)
+    const size_t step = (size_t)TB * p.D;
+    auto fetch = [&](long long t) {
+        if (t + TT <= end) {
+            size_t at = (size_t)(t + tok) * p.D;
+#pragma unroll
+            for (int e = 0; e < NB; ++e, at += step)
+#pragma unroll
+                for (int o = 0; o < OWN; ++o) {
+                    u[e][o] = p.u[at + own[o]];
+                    d[e][o] = p.delta[at + own[o]];
+                    if (gate) z[e][o] = p.z[at + own[o]];
+                }
+        } else {
+#pragma unroll
+            for (int e = 0; e < NB; ++e) {
+                const long long tt = t + e * TB + tok;
+                const size_t at = (size_t)(tt < end ? tt : end - 1) * p.D;
+#pragma unroll
+                for (int o = 0; o < OWN; ++o) {
+                    u[e][o] = p.u[at + own[o]];
+                    d[e][o] = p.delta[at + own[o]];
+                    if (gate) z[e][o] = p.z[at + own[o]];
+                }
+            }
+        }
+        bc.load(p, t, end, g, lane);
     };
 
-    fetch(t0);
-    stage(t0, 0);
-    u_now = u;
-    if (!kCarry && p.z) z_now = z;
-    if (t0 + TT < end) fetch(t0 + TT);
-    __syncthreads();
-    int buf = 0;
-    for (long long t = t0; t < end; t += TT, buf ^= 1) {
-        ChannelRows<T, Tl> u_next, z_next;
-        if (t + TT < end) {
-            stage(t + TT, buf ^ 1);
-            u_next = u;
-            if (!kCarry && p.z) z_next = z;
-            if (t + 2 * TT < end) fetch(t + 2 * TT);
-        }
-#pragma unroll 2
-        for (int tb = 0; tb < TT; tb += 4) {
-            float y[4];
+    if (t0 < end) fetch(t0);
+    for (long long t = t0; t < end; t += TT) {
+        const int left = end - t < TT ? (int)(end - t) : TT;
+        float x[NB][OWN], zz[NB][OWN], dt[NB * OWN];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 dd = s_dt[buf][tb + j][ch];
-                const float4 B = *reinterpret_cast<const float4*>(&s_B[buf][(tb + j) * SP + s0]);
-                const float2 dt = both(dd.x), du = both(dd.y);
-                h01 = fma2(ex2(mul2(dt, A01)), h01, mul2(du, make_float2(B.x, B.y)));
-                h23 = fma2(ex2(mul2(dt, A23)), h23, mul2(du, make_float2(B.z, B.w)));
-                if constexpr (!kCarry) {
-                    const float4 C = *reinterpret_cast<const float4*>(&s_C[buf][(tb + j) * SP + s0]);
-                    const float2 yy = fma2(h01, make_float2(C.x, C.y), mul2(h23, make_float2(C.z, C.w)));
-                    y[j] = yy.x + yy.y;
+        for (int e = 0; e < NB; ++e)
+#pragma unroll
+            for (int o = 0; o < OWN; ++o) {
+                float w[1];
+                load_vec<1>(&u[e][o], w);
+                x[e][o] = w[0];
+                load_vec<1>(&d[e][o], w);
+                dt[e * OWN + o] = w[0] + bias[o];
+                if (gate) {
+                    load_vec<1>(&z[e][o], w);
+                    zz[e][o] = w[0];
+                }
+            }
+        if (p.softplus) {
+            if constexpr (NB * OWN % 2 == 0) {
+#pragma unroll
+                for (int i = 0; i < NB * OWN; i += 2) {
+                    const float2 v = softplus2(make_float2(dt[i], dt[i + 1]));
+                    dt[i] = v.x;
+                    dt[i + 1] = v.y;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NB * OWN; ++i) dt[i] = softplus(dt[i]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < NB; ++e)
+#pragma unroll
+            for (int o = 0; o < OWN; ++o) {
+                const float v = e * TB + tok < left ? dt[e * OWN + o] : 0.f;  // behind the end: a step of nothing
+                if (kCarry) dt_sum[o] += v;
+                const float w = v * x[e][o];
+                s_dt[e * TB + tok][pair][OWN == 2 ? o : lane & 1] = make_float2(v, w);
+            }
+        bc.put(s_B, s_C, lane);
+        if (t + TT < end) fetch(t + TT);
+        __syncwarp();
+        // Two tokens ahead: what is read from shared memory; one ahead: the
+        // decays, so that neither's latency stands in the recurrence's way.
+        float4 dd[3], B[3], C[3];
+        float a[2][2][4];
+        auto read = [&](int tt) {
+            dd[tt % 3] = *reinterpret_cast<const float4*>(&s_dt[tt][pair][0]);
+            B[tt % 3] = *reinterpret_cast<const float4*>(&s_B[tt * SP + s0]);
+            if constexpr (!kCarry) C[tt % 3] = *reinterpret_cast<const float4*>(&s_C[tt * SP + s0]);
+        };
+        auto decay = [&](int tt) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[tt % 2][r][i] = ex2((r ? dd[tt % 3].z : dd[tt % 3].x) * A[r][i]);
+        };
+        read(0);
+        read(1);
+        decay(0);
+        size_t at = (size_t)(t + tok) * p.D;
+#pragma unroll
+        for (int e = 0; e < NB; ++e, at += step) {
+            float y[2 * TB];
+#pragma unroll
+            for (int j = 0; j < TB; ++j) {
+                const int tt = e * TB + j;
+                if (tt + 2 < TT) read(tt + 2);
+                if (tt + 1 < TT) decay(tt + 1);
+                const float4 b = B[tt % 3];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float du = r ? dd[tt % 3].w : dd[tt % 3].y;
+                    h[r][0] = fmaf(a[tt % 2][r][0], h[r][0], du * b.x);
+                    h[r][1] = fmaf(a[tt % 2][r][1], h[r][1], du * b.y);
+                    h[r][2] = fmaf(a[tt % 2][r][2], h[r][2], du * b.z);
+                    h[r][3] = fmaf(a[tt % 2][r][3], h[r][3], du * b.w);
+                    if constexpr (!kCarry) {
+                        const float4 c = C[tt % 3];
+                        y[r * TB + j] = fmaf(h[r][3], c.w, fmaf(h[r][2], c.z, fmaf(h[r][1], c.y, h[r][0] * c.x)));
+                    }
                 }
             }
             if constexpr (!kCarry) {
-                fold<4, L, 1>(y, lane);
-                constexpr int KEEP = L >= 4 ? 1 : 4 / L;      // tokens a lane is left with
-                constexpr int BITS = L >= 4 ? 2 : (L == 2 ? 1 : 0);
-                if (tid % L < 4) {
-                    const int at = fold_index<BITS>(lane, 1) * KEEP;
+                fold<2 * TB, L, 1>(y, lane);
 #pragma unroll
-                    for (int i = 0; i < KEEP; ++i) s_y[buf][(tb + at + i) * YP + ch] = y[i];
+                for (int o = 0; o < OWN; ++o) {
+                    float v[1] = {fmaf(skip[o], x[e][o], y[o])};
+                    if (gate) v[0] *= silu(zz[e][o]);
+                    if (mine[o] && e * TB + tok < left) store_vec<1>(p.out + at + own[o], v);
                 }
             }
         }
-        __syncthreads();
-        if constexpr (!kCarry) {
-#pragma unroll
-            for (int k = 0; k < IPT; ++k) {
-                const int tt = (tid + k * kThreads) / Q;
-                if (tt >= TT || t + tt >= end || q4 >= nch) continue;
-                const float4 y4 = *reinterpret_cast<const float4*>(&s_y[buf][tt * YP + q4]);
-                float x[4], zz[4], y[4] = {y4.x, y4.y, y4.z, y4.w};
-                u_now.r[k].get(x);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = fmaf(skip[i], x[i], y[i]);
-                if (p.z) {
-                    z_now.r[k].get(zz);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] *= silu(zz[i]);
-                }
-                store4(p.out + (size_t)(t + tt) * p.D + c0 + q4, y, p.vec_d, nch - q4);
-            }
-            u_now = u_next;
-            if (p.z) z_now = z_next;
-        }
+        __syncwarp();
     }
 
-    h[0] = h01.x;
-    h[1] = h01.y;
-    h[2] = h23.x;
-    h[3] = h23.y;
+    if (kCarry || (last && p.fin)) {
+        float* to = kCarry ? p.ends + (size_t)slot * p.D * p.S : p.fin + (size_t)n * p.D * p.S;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int c = pair * 2 + r;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (c < nch && s0 + i < p.S) to[(size_t)(c0 + c) * p.S + s0 + i] = h[r][i];
+        }
+    }
     if constexpr (kCarry) {
-        float* e = p.ends + (size_t)slot * p.D * p.S + row + s0;
+        // a channel's tokens lie with the lanes of its parity
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (chan && s0 + i < p.S) e[i] = h[i];
-        // sum of dt over the threads that staged a channel's tokens
-        float* red = reinterpret_cast<float*>(&s_dt[0][0][0]);
-        __syncthreads();
-        if (tid / Q < TT) {
+        for (int o = 0; o < OWN; ++o) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) red[(tid / Q) * CH + q4 + i] = dt_sum[i];
+            for (int i = 2; i < L; i <<= 1) dt_sum[o] += __shfl_xor_sync(0xffffffffu, dt_sum[o], i);
+            if (mine[o] && lane % L < 2) p.steps[(size_t)slot * p.D + own[o]] = dt_sum[o];
         }
-        __syncthreads();
-        if (tid < nch) {
-            float s = 0.f;
-            for (int r = 0; r < Tl::ROWS; ++r) s += red[r * CH + tid];
-            p.steps[(size_t)slot * p.D + c0 + tid] = s;
-        }
-    } else if (last && p.fin && chan) {
-        float* f = p.fin + (size_t)n * p.D * p.S + row + s0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (s0 + i < p.S) f[i] = h[i];
     }
 }
 
@@ -313,13 +360,25 @@ kda_ssm_step_kernel(const T* __restrict__ u, const T* __restrict__ delta, const 
 }
 
 // A unit's tokens are passed over twice where sequences are cut.
-constexpr int kWarps = 12, kShortest = 64;
+constexpr int kFewWarps = 6, kWantWarps = 12, kShortest = 64;
+
+// Lanes that share two channels, and warps of one sequence's channels.
+int fwd_lanes(int S)
+{
+    int l = 1;
+    while (4 * l < S) l <<= 1;
+    return l;
+}
+Cut fwd_cut(int B, int T, int D, int S, int N, int packed)
+{
+    return cut_of(B, T, N, packed, (double)D * fwd_lanes(S) / 64.0, kFewWarps, kWantWarps, kShortest);
+}
 
 template <typename T, int L>
 cudaError_t fwd(const ScanArgs& a, cudaStream_t st)
 {
-    const Cut c = cut_of(a.B, a.T, a.D, a.S, a.N, a.cu_seqlens != nullptr, kWarps, kShortest);
-    Params<T> p = params_of<T>(a, c.len, Tile<L>::CH);
+    const Cut c = fwd_cut(a.B, a.T, a.D, a.S, a.N, a.cu_seqlens != nullptr);
+    Params<T> p = params_of<T>(a, c.len, Fwd<L>::CH);
     const long long slots = p.units.slots();
     const long long blocks = slots * p.G * p.cpb;
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
@@ -327,11 +386,11 @@ cudaError_t fwd(const ScanArgs& a, cudaStream_t st)
     if (c.cut) {
         p.ends = (float*)a.workspace;
         p.steps = (float*)((char*)a.workspace + round256((size_t)slots * a.D * a.S * 4));
-        kda_ssm_scan_kernel<T, L, true><<<(unsigned)blocks, kThreads, 0, st>>>(p);
+        kda_ssm_scan_kernel<T, L, true><<<(unsigned)blocks, 32, 0, st>>>(p);
         if (cudaError_t e = cudaGetLastError()) return e;
         if (cudaError_t e = launch_ssm_chain(a.A, a.initial_state, p.ends, p.steps, p.units, a.D, a.S, st)) return e;
     }
-    kda_ssm_scan_kernel<T, L, false><<<(unsigned)blocks, kThreads, 0, st>>>(p);
+    kda_ssm_scan_kernel<T, L, false><<<(unsigned)blocks, 32, 0, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -353,22 +412,29 @@ cudaError_t step(const ScanArgs& a, cudaStream_t st)
     return cudaGetLastError();
 }
 
-template <typename T, bool kStep>
-cudaError_t by_states(const ScanArgs& a, cudaStream_t st)
+template <typename T>
+cudaError_t fwd_by_states(const ScanArgs& a, cudaStream_t st)
 {
-    switch (lanes_of(a.S)) {
-#define KDA_SSM_L(L) \
-    case L:          \
-        return kStep ? step<T, L>(a, st) : fwd<T, L>(a, st);
-        KDA_SSM_L(1)
-        KDA_SSM_L(2)
-        KDA_SSM_L(4)
-        KDA_SSM_L(8)
-        KDA_SSM_L(16)
-        KDA_SSM_L(32)
-#undef KDA_SSM_L
+    switch (fwd_lanes(a.S)) {
+        case 1: return fwd<T, 1>(a, st);
+        case 2: return fwd<T, 2>(a, st);
+        case 4: return fwd<T, 4>(a, st);
+        case 8: return fwd<T, 8>(a, st);
+        case 16: return fwd<T, 16>(a, st);
+        case 32: return fwd<T, 32>(a, st);
     }
     return cudaErrorInvalidValue;
+}
+
+template <typename T>
+cudaError_t step_by_states(const ScanArgs& a, cudaStream_t st)
+{
+    if (a.S <= 4) return step<T, 1>(a, st);
+    if (a.S <= 8) return step<T, 2>(a, st);
+    if (a.S <= 16) return step<T, 4>(a, st);
+    if (a.S <= 32) return step<T, 8>(a, st);
+    if (a.S <= 64) return step<T, 16>(a, st);
+    return step<T, 32>(a, st);
 }
 
 }  // namespace
@@ -386,7 +452,7 @@ cudaError_t launch_ssm_chain(const float* A, const float* init, float* ends, con
 
 size_t scan_fwd_workspace(int B, int T, int D, int S, int, int N, int packed, kda_dtype)
 {
-    const Cut c = cut_of(B, T, D, S, N, packed, kWarps, kShortest);
+    const Cut c = fwd_cut(B, T, D, S, N, packed);
     if (!c.cut) return 0;
     const size_t slots = (size_t)slots_of(B, T, N, packed, c.len);
     return round256(slots * D * S * 4) + slots * D * 4;
@@ -394,12 +460,12 @@ size_t scan_fwd_workspace(int B, int T, int D, int S, int, int N, int packed, kd
 
 cudaError_t launch_scan_fwd(const ScanArgs& a, kda_dtype dtype, cudaStream_t st)
 {
-    return dtype == KDA_DTYPE_BF16 ? by_states<__nv_bfloat16, false>(a, st) : by_states<float, false>(a, st);
+    return dtype == KDA_DTYPE_BF16 ? fwd_by_states<__nv_bfloat16>(a, st) : fwd_by_states<float>(a, st);
 }
 
 cudaError_t launch_scan_step(const ScanArgs& a, kda_dtype dtype, cudaStream_t st)
 {
-    return dtype == KDA_DTYPE_BF16 ? by_states<__nv_bfloat16, true>(a, st) : by_states<float, true>(a, st);
+    return dtype == KDA_DTYPE_BF16 ? step_by_states<__nv_bfloat16>(a, st) : step_by_states<float>(a, st);
 }
 
 }  // namespace kda
