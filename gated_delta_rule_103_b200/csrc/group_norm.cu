@@ -12,11 +12,10 @@
 // and the normalisation (x is read twice; what fits the 126 MB L2 comes from
 // HBM once).
 //
-// Statistics are held as (count, mean, sum of squared deviations) and merged
-// pairwise by
-//     m = m1 + (m2 - m1) n2 / n,   q = q1 + q2 + (m2 - m1)^2 n1 n2 / n
-// so that a mean far from zero costs no digits; within a thread the sums run
-// over x - k with k the thread's first value.
+// Sums of squares run over deviations: within a thread from the thread's first
+// value, across threads and units from the common mean,
+//     q = sum_i (q_i + n_i (m_i - m)^2),
+// so that a mean far from zero costs no digits.
 #include "layer.h"
 #include "layer_common.cuh"
 
@@ -25,24 +24,18 @@ namespace {
 
 using namespace layer;
 
-struct Moments {
-    float n, m, q;
-    __device__ __forceinline__ void merge(const Moments& o)
-    {
-        const float t = n + o.n;
-        if (t <= 0.f) return;
-        const float d = o.m - m, r = o.n / t;
-        m = fmaf(d, r, m);
-        q += o.q + d * d * n * r;
-        n = t;
-    }
-};
-
 template <int LANES>
 __device__ __forceinline__ float lane_sum(float v)
 {
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Sum over groups of `lanes` neighbouring lanes (a power of two).
+__device__ __forceinline__ float part_sum(float v, int lanes)
+{
+    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
@@ -305,9 +298,9 @@ struct Layout {
 // One unit's tokens of the column at p, ty apart, kBatch rows in flight.
 constexpr int kBatch = 8;
 template <typename T, int V, typename F>
-__device__ __forceinline__ void each_token(const T* p, long long a, long long b, int C, int ty, F&& f)
+__device__ __forceinline__ void each_token(const T* p, int a, int b, int C, int ty, F&& f)
 {
-    for (long long t = a; t < b; t += (long long)kBatch * ty) {
+    for (int t = a; t < b; t += kBatch * ty) {
         Raw<T, V> r[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
@@ -323,10 +316,10 @@ __device__ __forceinline__ void each_token(const T* p, long long a, long long b,
 }
 // ... of the columns at p and q
 template <typename T, int V, typename F>
-__device__ __forceinline__ void each_token2(const T* p, const T* q, long long a, long long b, int C, int ty, F&& f)
+__device__ __forceinline__ void each_token2(const T* p, const T* q, int a, int b, int C, int ty, F&& f)
 {
     constexpr int U = kBatch / 2;
-    for (long long t = a; t < b; t += (long long)U * ty) {
+    for (int t = a; t < b; t += U * ty) {
         Raw<T, V> r[U], s[U];
 #pragma unroll
         for (int i = 0; i < U; ++i)
@@ -351,24 +344,25 @@ template <typename T, int V>
 __global__ void __launch_bounds__(256)
 kda_norm_stats_kernel(const T* __restrict__ x, float* __restrict__ part, Units units, Layout l, int C, int G)
 {
-    __shared__ float sn[256], sm[256], sq[256];
-    int n, seg;
-    long long a, b;
-    const long long unit = blockIdx.x / l.ngb;
-    if (!units.locate(unit, n, seg, a, b)) return;
+    __shared__ float sn[256], sm[256], sq[256];  // per thread: count, mean, squared deviations
+    int n, seg, a, b;
+    bool last;
+    const int unit = blockIdx.x / l.ngb;
+    if (!units.locate(unit, n, seg, last, a, b)) return;
     const int g0 = (int)(blockIdx.x % l.ngb) * l.gb;
     const int groups = G - g0 < l.gb ? G - g0 : l.gb;
     const int wide = l.cols > 256;
     const int ty = wide ? 0 : threadIdx.x / l.cols;
     const int cx = wide ? threadIdx.x : threadIdx.x % l.cols;
-    Moments mo = {0.f, 0.f, 0.f};
+    float cnt = 0.f, mean = 0.f, dev = 0.f;
     if (ty < l.ty && a + ty < b) {
+        const float rows = (float)((b - a - ty + l.ty - 1) / l.ty * V);
         for (int c = cx; c < groups * l.cpg; c += wide ? 256 : l.cols) {
             const T* p = x + ((size_t)g0 * l.cpg + c) * V;
             float first[V], s1 = 0.f, s2 = 0.f;
             load_vec<V>(p + (size_t)(a + ty) * C, first);
             const float k = first[0];
-            each_token<T, V>(p, a + ty, b, C, l.ty, [&](long long, const float (&v)[V]) {
+            each_token<T, V>(p, a + ty, b, C, l.ty, [&](int, const float (&v)[V]) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const float d = v[j] - k;
@@ -376,32 +370,42 @@ kda_norm_stats_kernel(const T* __restrict__ x, float* __restrict__ part, Units u
                     s2 = fmaf(d, d, s2);
                 }
             });
-            const float cnt = (float)((b - a - ty + l.ty - 1) / l.ty * V), d = s1 / cnt;
-            const Moments o = {cnt, k + d, fmaxf(s2 - s1 * d, 0.f)};
-            mo.merge(o);
+            const float d = s1 / rows, m = k + d, q = fmaxf(s2 - s1 * d, 0.f);
+            // another column of the same group (wide): shares by the counts
+            const float all = cnt + rows, r = rows / all, e = m - mean;
+            dev += q + e * e * cnt * r;
+            mean = fmaf(e, r, mean);
+            cnt = all;
         }
     }
-    sn[threadIdx.x] = mo.n;
-    sm[threadIdx.x] = mo.m;
-    sq[threadIdx.x] = mo.q;
+    sn[threadIdx.x] = cnt;
+    sm[threadIdx.x] = mean;
+    sq[threadIdx.x] = dev;
     __syncthreads();
-    // a warp per group: its threads' moments lane by lane, then across lanes
-    const int lane = threadIdx.x & 31;
-    for (int g = threadIdx.x >> 5; g < groups; g += l.threads / 32) {
-        const int per = wide ? 256 : l.cpg * l.ty;
-        Moments t = {0.f, 0.f, 0.f};
-        for (int i = lane; i < per; i += 32) {
-            const int src = wide ? i : (i / l.cpg) * l.cols + g * l.cpg + i % l.cpg;
-            const Moments o = {sn[src], sm[src], sq[src]};
-            t.merge(o);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const Moments u = {__shfl_xor_sync(0xffffffffu, t.n, o), __shfl_xor_sync(0xffffffffu, t.m, o),
-                               __shfl_xor_sync(0xffffffffu, t.q, o)};
-            t.merge(u);
-        }
-        if (lane == 0) *reinterpret_cast<float2*>(part + ((size_t)unit * G + g0 + g) * 2) = make_float2(t.m, t.q);
+    // over a group's threads: `lg` lanes a group
+    const int per = wide ? 256 : l.cpg * l.ty;
+    int lg = 32;
+    while (lg > 1 && lg / 2 >= per) lg >>= 1;
+    const int sub = threadIdx.x % lg, across = l.threads / lg;
+    const float inv = 1.f / ((float)(b - a) * (float)(l.cpg * V));
+    for (int g1 = 0; g1 < groups; g1 += across) {
+        const int g = g1 + threadIdx.x / lg;
+        auto at = [&](int i) { return wide ? i : (i / l.cpg) * l.cols + g * l.cpg + i % l.cpg; };
+        const float k = g < groups ? sm[at(0)] : 0.f;
+        float s1 = 0.f, s2 = 0.f, rest = 0.f;
+        if (g < groups)
+            for (int i = sub; i < per; i += lg) s1 = fmaf(sn[at(i)], sm[at(i)] - k, s1);
+        float m = fmaf(part_sum(s1, lg), inv, k);
+        if (g < groups)
+            for (int i = sub; i < per; i += lg) {
+                const float e = sm[at(i)] - m;
+                rest = fmaf(sn[at(i)], e, rest);  // what k's rounding left of the mean
+                s2 += fmaf(sn[at(i)] * e, e, sq[at(i)]);
+            }
+        s2 = part_sum(s2, lg);
+        m = fmaf(part_sum(rest, lg), inv, m);
+        if (g < groups && sub == 0)
+            *reinterpret_cast<float2*>(part + ((size_t)unit * G + g0 + g) * 2) = make_float2(m, s2);
     }
 }
 
@@ -414,26 +418,31 @@ kda_norm_merge_kernel(const float* __restrict__ part, float* __restrict__ mean, 
     const int lane = threadIdx.x & 31;
     if (id >= (long long)units.s.N * G) return;
     const int n = (int)(id / G), g = (int)(id % G);
-    long long a, b;
+    int a, b;
     units.s.bounds(n, a, b);
-    const long long first = units.first(n);
-    const int cnt = units.count(n);
-    Moments t = {0.f, 0.f, 0.f};
-    for (int i = lane; i < cnt; i += 32) {
-        const long long left = b - a - (long long)i * units.len;
-        const float2 p = *reinterpret_cast<const float2*>(part + ((size_t)(first + i) * G + g) * 2);
-        const Moments o = {(float)(left < units.len ? left : units.len) * (float)Cg, p.x, p.y};
-        t.merge(o);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const Moments u = {__shfl_xor_sync(0xffffffffu, t.n, o), __shfl_xor_sync(0xffffffffu, t.m, o),
-                           __shfl_xor_sync(0xffffffffu, t.q, o)};
-        t.merge(u);
-    }
+    const int cnt = units.count_of(a, b);
+    const float* p = part + ((size_t)units.first(n) * G + g) * 2;
+    const float inv = b > a ? 1.f / ((float)(b - a) * (float)Cg) : 0.f;
+    const float k = b > a ? p[0] : 0.f;
+    float s1 = 0.f, s2 = 0.f, rest = 0.f;
+    auto weight = [&](int i) {  // values of unit i
+        const int left = b - a - i * units.len;
+        return (float)(left < units.len ? left : units.len) * (float)Cg;
+    };
+    if (b > a)
+        for (int i = lane; i < cnt; i += 32) s1 = fmaf(weight(i), p[(size_t)i * G * 2] - k, s1);
+    float m = fmaf(lane_sum<32>(s1), inv, k);
+    if (b > a)
+        for (int i = lane; i < cnt; i += 32) {
+            const float e = p[(size_t)i * G * 2] - m;
+            rest = fmaf(weight(i), e, rest);  // what k's rounding left of the mean
+            s2 += fmaf(weight(i) * e, e, p[(size_t)i * G * 2 + 1]);
+        }
+    s2 = lane_sum<32>(s2);
+    m = fmaf(lane_sum<32>(rest), inv, m);
     if (lane == 0) {
-        mean[id] = t.m;  // 0 of an empty sequence
-        rstd[id] = 1.f / sqrtf((t.n > 0.f ? t.q / t.n : 0.f) + eps);
+        mean[id] = m;  // 0 of an empty sequence
+        rstd[id] = 1.f / sqrtf(fmaf(s2, inv, eps));
     }
 }
 
@@ -446,9 +455,9 @@ kda_norm_apply_kernel(const T* __restrict__ x, const float* __restrict__ weight,
                       const T* __restrict__ d_out, const float* __restrict__ sums, float* __restrict__ grad_x,
                       Units units, Layout l, int C, int G, int act)
 {
-    int n, seg;
-    long long a, b;
-    if (!units.locate(blockIdx.x / l.ngb, n, seg, a, b)) return;
+    int n, seg, a, b;
+    bool last;
+    if (!units.locate(blockIdx.x / l.ngb, n, seg, last, a, b)) return;
     const int g0 = (int)(blockIdx.x % l.ngb) * l.gb;
     const int groups = G - g0 < l.gb ? G - g0 : l.gb;
     const int wide = l.cols > 256;
@@ -466,7 +475,7 @@ kda_norm_apply_kernel(const T* __restrict__ x, const float* __restrict__ weight,
             bb[j] = bias ? bias[ch + j] : 0.f;
         }
         if constexpr (!kBwd) {
-            each_token<T, V>(x + ch, a + ty, b, C, l.ty, [&](long long t, float (&v)[V]) {
+            each_token<T, V>(x + ch, a + ty, b, C, l.ty, [&](int t, float (&v)[V]) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     v[j] = fmaf((v[j] - m) * rs, w[j], bb[j]);
@@ -476,7 +485,7 @@ kda_norm_apply_kernel(const T* __restrict__ x, const float* __restrict__ weight,
             });
         } else {
             const float k1 = sums[ng * 2], k2 = sums[ng * 2 + 1];
-            each_token2<T, V>(x + ch, d_out + ch, a + ty, b, C, l.ty, [&](long long t, float (&v)[V], float (&dy)[V]) {
+            each_token2<T, V>(x + ch, d_out + ch, a + ty, b, C, l.ty, [&](int t, float (&v)[V], float (&dy)[V]) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const float xh = (v[j] - m) * rs;
@@ -500,17 +509,16 @@ kda_norm_bwd_sums_kernel(const T* __restrict__ x, const float* __restrict__ weig
                          Units units, Layout l, int C, int G, int act)
 {
     __shared__ float red[2 * V * 256];  // per thread, then [2][channels] of the block
-    int n, seg;
-    long long a, b;
-    const long long unit = blockIdx.x / l.ngb;
+    int n, seg, a, b;
+    bool last;
+    const int unit = blockIdx.x / l.ngb;
     const int g0 = (int)(blockIdx.x % l.ngb) * l.gb;
     const int groups = G - g0 < l.gb ? G - g0 : l.gb;
     const int wide = l.cols > 256;
     const int chans = groups * l.cpg * V, ch0 = g0 * l.cpg * V;
-    const int lane = threadIdx.x & 31;
     float* pw = part + ((size_t)unit * 2) * C + ch0;
     float* pb = pw + C;
-    if (!units.locate(unit, n, seg, a, b)) {
+    if (!units.locate(unit, n, seg, last, a, b)) {
         for (int c = threadIdx.x; c < chans; c += l.threads) pw[c] = pb[c] = 0.f;
         return;
     }
@@ -529,7 +537,7 @@ kda_norm_bwd_sums_kernel(const T* __restrict__ x, const float* __restrict__ weig
             bb[j] = bias ? bias[ch + j] : 0.f;
             dw[j] = db[j] = 0.f;
         }
-        each_token2<T, V>(x + ch, d_out + ch, a + ty, b, C, l.ty, [&](long long, float (&v)[V], float (&dy)[V]) {
+        each_token2<T, V>(x + ch, d_out + ch, a + ty, b, C, l.ty, [&](int, float (&v)[V], float (&dy)[V]) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float xh = (v[j] - m) * rs;
@@ -576,17 +584,24 @@ kda_norm_bwd_sums_kernel(const T* __restrict__ x, const float* __restrict__ weig
         pw[c] = red[(c % V) * 256 + c / V];
         pb[c] = red[(V + c % V) * 256 + c / V];
     }
-    for (int g = threadIdx.x >> 5; g < groups; g += l.threads / 32) {
+    const int per = l.cpg * V;
+    int lg = 32;
+    while (lg > 1 && lg / 2 >= per) lg >>= 1;
+    const int sub = threadIdx.x % lg;
+    for (int g1 = 0; g1 < groups; g1 += l.threads / lg) {
+        const int g = g1 + threadIdx.x / lg;
         float t1 = 0.f, t2 = 0.f;
-        for (int i = lane; i < l.cpg * V; i += 32) {
-            const int c = g * l.cpg * V + i;
-            const float w = weight ? weight[ch0 + c] : 1.f;
-            t1 = fmaf(w, red[(V + c % V) * 256 + c / V], t1);
-            t2 = fmaf(w, red[(c % V) * 256 + c / V], t2);
-        }
-        t1 = lane_sum<32>(t1);
-        t2 = lane_sum<32>(t2);
-        if (lane == 0) *reinterpret_cast<float2*>(gsum + ((size_t)unit * G + g0 + g) * 2) = make_float2(t1, t2);
+        if (g < groups)
+            for (int i = sub; i < per; i += lg) {
+                const int c = g * per + i;
+                const float w = weight ? weight[ch0 + c] : 1.f;
+                t1 = fmaf(w, red[(V + c % V) * 256 + c / V], t1);
+                t2 = fmaf(w, red[(c % V) * 256 + c / V], t2);
+            }
+        t1 = part_sum(t1, lg);
+        t2 = part_sum(t2, lg);
+        if (g < groups && sub == 0)
+            *reinterpret_cast<float2*>(gsum + ((size_t)unit * G + g0 + g) * 2) = make_float2(t1, t2);
     }
 }
 
@@ -624,10 +639,9 @@ kda_norm_bwd_merge_kernel(const float* __restrict__ part, float* __restrict__ gr
     const long long id = (long long)(blockIdx.x - param_blocks) * 32 + y;
     if (id >= (long long)units.s.N * G) return;
     const int n = (int)(id / G), g = (int)(id % G);
-    long long a, b;
+    int a, b;
     units.s.bounds(n, a, b);
-    const long long first = units.first(n);
-    const int cnt = units.count(n);
+    const int first = units.first(n), cnt = units.count_of(a, b);
     float s1 = 0.f, s2 = 0.f;
     for (int i = lane; i < cnt; i += 32) {
         const float2 p = *reinterpret_cast<const float2*>(gsum + ((size_t)(first + i) * G + g) * 2);
@@ -681,7 +695,7 @@ Units units_of(const int32_t* cu, int B, int T, int N, int len)
     u.s.cu = cu;
     u.s.N = N;
     u.s.T = T;
-    u.s.total = (long long)B * T;
+    u.s.total = B * T;
     u.len = len;
     u.per_seq = T > 0 ? (T + len - 1) / len : 1;
     return u;
@@ -764,7 +778,7 @@ cudaError_t forward(const NormArgs& a, kda_dtype dtype, cudaStream_t st)
     }
     const Layout l = layout_of(a.C, a.G, V, (long long)a.B * a.T);
     const Units u = units_of(a.cu_seqlens, a.B, a.T, a.N, l.len);
-    const long long blocks = u.slots() * l.ngb, ng = (long long)a.N * a.G;
+    const long long blocks = (long long)u.slots() * l.ngb, ng = (long long)a.N * a.G;
     if (blocks > INT32_MAX || (ng + 7) / 8 > INT32_MAX) return cudaErrorInvalidConfiguration;
     float* part = (float*)a.workspace;
     if (blocks > 0) {

@@ -54,7 +54,7 @@ private:
     bool ok_ = true;
 };
 
-constexpr size_t kMostTokens = (size_t)INT32_MAX;
+constexpr size_t kMostTokens = (size_t)1 << 30;  // and sequences
 constexpr int kMostChannels = 1 << 24;
 
 // Sizes that every call over sequences shares; KDA_OK: go on.
@@ -67,7 +67,8 @@ kda_status check_sizes(int B, int T, int C, int N, const void* cu, kda_dtype dty
     } else if (N != B) {
         return KDA_ERR_INVALID_ARG;
     }
-    if ((size_t)B * (size_t)T > kMostTokens || C > kMostChannels) return KDA_ERR_UNSUPPORTED;
+    if ((size_t)B * (size_t)T > kMostTokens || (size_t)N > kMostTokens || C > kMostChannels)
+        return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -96,7 +97,7 @@ kda_status check_scan(int D, int S, int G, unsigned flags)
 bool sizes_ok(int B, int T, int C, int N, int packed)
 {
     return B >= 0 && T >= 0 && C > 0 && N >= 0 && (packed ? B == 1 && !(N == 0 && T > 0) : N == B) &&
-           (size_t)B * (size_t)T <= kMostTokens && C <= kMostChannels;
+           (size_t)B * (size_t)T <= kMostTokens && (size_t)N <= kMostTokens && C <= kMostChannels;
 }
 
 bool dtype_ok(kda_dtype d) { return d == KDA_DTYPE_F32 || d == KDA_DTYPE_BF16; }

@@ -127,28 +127,29 @@ __device__ __forceinline__ float silu_slope(float v)
 // The sequences of a call: N sequences of T tokens each, or, packed, sequence
 // n at tokens [cu[n], cu[n + 1]) of `total`.  Bounds are held to [0, total],
 // so that an array that breaks the contract gives wrong values and no access
-// out of range.
+// out of range.  (Up to 2^30 tokens and sequences: a token's number, and that of
+// a unit below, fits an int.)
 struct Seqs {
     const int32_t* cu;
     int N;
     int T;
-    long long total;
-    __device__ __forceinline__ long long start(int n) const
+    int total;
+    __device__ __forceinline__ int start(int n) const
     {
-        if (!cu) return (long long)n * T;
-        const long long s = cu[n];
+        if (!cu) return n * T;
+        const int s = cu[n];
         return s < 0 ? 0 : (s > total ? total : s);
     }
-    __device__ __forceinline__ void bounds(int n, long long& a, long long& b) const
+    __device__ __forceinline__ void bounds(int n, int& a, int& b) const
     {
         a = start(n);
         b = cu ? start(n + 1) : a + T;
         if (b < a) b = a;
     }
     // the last sequence that begins at or before token t
-    __device__ __forceinline__ int find(long long t) const
+    __device__ __forceinline__ int find(int t) const
     {
-        if (!cu) return T > 0 ? (int)(t / T) : 0;
+        if (!cu) return T > 0 ? (int)((unsigned)t / (unsigned)T) : 0;
         int lo = 0, len = N;
         while (len > 1) {
             const int half = len >> 1;
@@ -171,30 +172,32 @@ struct Units {
     Seqs s;
     int len;
     int per_seq;  // units of a sequence that is not packed
-    __host__ __device__ long long slots() const
+    __host__ __device__ int slots() const { return s.cu ? s.total / len + s.N : s.N * per_seq; }
+    __device__ __forceinline__ int first(int n) const
     {
-        return s.cu ? s.total / len + s.N : (long long)s.N * per_seq;
+        return s.cu ? (int)((unsigned)s.start(n) / (unsigned)len) + n : n * per_seq;
     }
-    __device__ __forceinline__ long long first(int n) const
+    __device__ __forceinline__ int count_of(int a, int b) const
     {
-        return s.cu ? s.start(n) / len + n : (long long)n * per_seq;
+        return b > a ? (int)((unsigned)(b - a + len - 1) / (unsigned)len) : 1;
     }
     __device__ __forceinline__ int count(int n) const
     {
         if (!s.cu) return per_seq;
-        long long a, b;
+        int a, b;
         s.bounds(n, a, b);
-        return b > a ? (int)((b - a + len - 1) / len) : 1;
+        return count_of(a, b);
     }
-    // Sequence, index and tokens [a, b) of slot j; false: an empty slot.
-    // Called by whole warps.
-    __device__ __forceinline__ bool locate(long long j, int& n, int& seg, long long& a, long long& b) const
+    // Sequence, index, whether it is the sequence's last, and tokens [a, b) of
+    // slot j; false: an empty slot.  Called by whole warps.
+    __device__ __forceinline__ bool locate(int j, int& n, int& seg, bool& last, int& a, int& b) const
     {
         if (!s.cu) {
-            n = (int)(j / per_seq);
-            seg = (int)(j - (long long)n * per_seq);
-            const long long s0 = (long long)n * s.T;
-            a = s0 + (long long)seg * len;
+            n = (int)((unsigned)j / (unsigned)per_seq);
+            seg = j - n * per_seq;
+            last = seg + 1 == per_seq;
+            const int s0 = n * s.T;
+            a = s0 + seg * len;
             b = a + len < s0 + s.T ? a + len : s0 + s.T;
             return true;
         }
@@ -203,19 +206,19 @@ struct Units {
         int lo = 0, cnt = s.N;
         while (cnt > 1) {
             const int step = (cnt + 31) >> 5;
-            const int i = lo + lane * step;
-            const bool ok = lane * step < cnt && first(i) <= j;
+            const bool ok = lane * step < cnt && first(lo + lane * step) <= j;
             const int hits = __popc(__ballot_sync(0xffffffffu, ok));
             const int at = (hits > 0 ? hits - 1 : 0) * step;
             lo += at;
             cnt = cnt - at < step ? cnt - at : step;
         }
         n = lo;
-        long long s0, s1;
+        int s0, s1;
         s.bounds(n, s0, s1);
-        const long long k = j - first(n);
-        if (k < 0 || k >= count(n)) return false;
-        seg = (int)k;
+        const int k = j - ((int)((unsigned)s0 / (unsigned)len) + n), all = count_of(s0, s1);
+        if (k < 0 || k >= all) return false;
+        seg = k;
+        last = k + 1 == all;
         a = s0 + k * len;
         b = a + len < s1 ? a + len : s1;
         return true;

@@ -61,7 +61,7 @@ __device__ __forceinline__ void push(float (&h)[W - 1][V], const float (&cur)[V]
 // Rows of (state ++ x) of sequence n: row r < W - 1 is the state's, row
 // W - 1 + p is token p.
 template <typename T, int W, int V>
-__device__ __forceinline__ void ext_row(const T* x, const T* state, int n, long long a, long long r, int C,
+__device__ __forceinline__ void ext_row(const T* x, const T* state, int n, int a, int r, int C,
                                         int c0, float (&v)[V])
 {
     if (r >= W - 1) {
@@ -78,26 +78,26 @@ template <typename T, int W, int V>
 __global__ void __launch_bounds__(128)
 kda_short_conv_kernel(const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
                       const T* state, T* __restrict__ out, T* fin, Seqs seqs, int C, int ncb,
-                      long long tiles, int run, int act)
+                      int tiles, int run, int act)
 {
     const int c0 = ((int)(blockIdx.x % ncb) * blockDim.x + threadIdx.x) * V;
-    const long long item = blockIdx.x / ncb;
+    const int item = blockIdx.x / ncb;
     if (c0 >= C) return;
     Taps<W, V> taps;
     taps.load(weight, bias, c0);
 
     if (item >= tiles) {
         // the first rows of a sequence, and its final state
-        const long long n = (item - tiles) * blockDim.y + threadIdx.y;
+        const int n = (item - tiles) * blockDim.y + threadIdx.y;
         if (n >= seqs.N) return;
-        long long a, b;
-        seqs.bounds((int)n, a, b);
-        const long long L = b - a;
+        int a, b;
+        seqs.bounds(n, a, b);
+        const int L = b - a;
         float h[W - 1][V], last[W - 1][V];
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
-            ext_row<T, W, V>(x, state, (int)n, a, j, C, c0, h[j]);
-            if (fin) ext_row<T, W, V>(x, state, (int)n, a, L + j, C, c0, last[j]);
+            ext_row<T, W, V>(x, state, n, a, j, C, c0, h[j]);
+            if (fin) ext_row<T, W, V>(x, state, n, a, L + j, C, c0, last[j]);
         }
 #pragma unroll
         for (int p = 0; p < W - 1; ++p) {
@@ -119,13 +119,13 @@ kda_short_conv_kernel(const T* __restrict__ x, const float* __restrict__ weight,
         return;
     }
 
-    long long t = (item * blockDim.y + threadIdx.y) * run;
-    const long long end = t + run < seqs.total ? t + run : seqs.total;
+    int t = (item * blockDim.y + threadIdx.y) * run;
+    const int end = t + run < seqs.total ? t + run : seqs.total;
     if (t >= end) return;
     for (int n = seqs.find(t); t < end && n < seqs.N; ++n) {
-        long long a, b;
+        int a, b;
         seqs.bounds(n, a, b);
-        const long long stop = b < end ? b : end;
+        const int stop = b < end ? b : end;
         if (t < a + W - 1) t = a + W - 1;
         if (t >= stop) {
             t = stop;
@@ -182,7 +182,7 @@ kda_short_conv_step_kernel(const T* __restrict__ x, const float* __restrict__ we
                            int act)
 {
     const int c0 = ((int)(blockIdx.x % ncb) * blockDim.x + threadIdx.x) * V;
-    const long long n = (long long)(blockIdx.x / ncb) * blockDim.y + threadIdx.y;
+    const int n = (int)(blockIdx.x / ncb) * blockDim.y + threadIdx.y;
     if (c0 >= C || n >= N) return;
     T* st = state + (size_t)n * (W - 1) * C + c0;
     float h[W - 1][V], cur[V], v[V];
@@ -216,26 +216,26 @@ kda_short_conv_bwd_kernel(const T* __restrict__ x, const float* __restrict__ wei
                           const float* __restrict__ bias, const T* __restrict__ state,
                           const T* __restrict__ d_out, const float* __restrict__ d_fin,
                           float* __restrict__ grad_x, float* __restrict__ grad_state, float* __restrict__ part,
-                          Seqs seqs, int C, int ncb, long long tiles, int run, int act)
+                          Seqs seqs, int C, int ncb, int tiles, int run, int act)
 {
     extern __shared__ float red[];  // [blockDim.y][(W + 1) * V][blockDim.x]
     const int c0 = ((int)(blockIdx.x % ncb) * blockDim.x + threadIdx.x) * V;
-    const long long item = blockIdx.x / ncb;
+    const int item = blockIdx.x / ncb;
     const bool mine = c0 < C;
     Taps<W, V> taps;
     if (mine) taps.load(weight, bias, c0);
 
     if (item >= tiles) {
         // the initial state's gradient
-        const long long n = (item - tiles) * blockDim.y + threadIdx.y;
+        const int n = (item - tiles) * blockDim.y + threadIdx.y;
         if (!mine || n >= seqs.N) return;
-        long long a, b;
-        seqs.bounds((int)n, a, b);
-        const long long L = b - a;
+        int a, b;
+        seqs.bounds(n, a, b);
+        const int L = b - a;
         float h[W - 1][V], dst[W - 1][V];
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
-            ext_row<T, W, V>(x, state, (int)n, a, j, C, c0, h[j]);
+            ext_row<T, W, V>(x, state, n, a, j, C, c0, h[j]);
 #pragma unroll
             for (int i = 0; i < V; ++i) dst[j][i] = 0.f;
             if (j >= L && d_fin) load_vec<V>(d_fin + ((size_t)n * (W - 1) + (j - L)) * C + c0, dst[j]);
@@ -267,13 +267,13 @@ kda_short_conv_bwd_kernel(const T* __restrict__ x, const float* __restrict__ wei
 #pragma unroll
         for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
     }
-    long long t0 = (item * blockDim.y + threadIdx.y) * run;
-    const long long end = t0 + run < seqs.total ? t0 + run : seqs.total;
+    int t0 = (item * blockDim.y + threadIdx.y) * run;
+    const int end = t0 + run < seqs.total ? t0 + run : seqs.total;
     if (mine && t0 < end) {
         for (int n = seqs.find(t0); t0 < end && n < seqs.N; ++n) {
-            long long a, b;
+            int a, b;
             seqs.bounds(n, a, b);
-            const long long stop = b < end ? b : end;
+            const int stop = b < end ? b : end;
             if (t0 < a) t0 = a;
             if (t0 >= stop) continue;
             float h[W - 1][V], part_dx[W - 1][V];  // part_dx[i]: what row t - (W - 1) + i has so far
@@ -284,7 +284,7 @@ kda_short_conv_bwd_kernel(const T* __restrict__ x, const float* __restrict__ wei
                 for (int i = 0; i < V; ++i) part_dx[j][i] = 0.f;
             }
             constexpr int U = 4;  // rows of x and of dy in flight per thread
-            for (long long t = t0; t < stop + W - 1; t += U) {
+            for (int t = t0; t < stop + W - 1; t += U) {
                 Raw<T, V> rx[U], rd[U];
 #pragma unroll
                 for (int k = 0; k < U; ++k)
@@ -327,9 +327,9 @@ kda_short_conv_bwd_kernel(const T* __restrict__ x, const float* __restrict__ wei
                         for (int j = 0; j + 1 < W - 1; ++j) part_dx[j][i] = fmaf(taps.w[j + 1][i], dv[i], part_dx[j + 1][i]);
                         part_dx[W - 2][i] = taps.w[W - 1][i] * dv[i];
                     }
-                    const long long p = t + k - (W - 1);
+                    const int p = t + k - (W - 1);
                     if (p >= t0) {
-                        const long long r = p - b + (W - 1);  // row of the final state
+                        const int r = p - b + (W - 1);  // row of the final state
                         if (r >= 0 && d_fin) {
                             float f[V];
                             load_vec<V>(d_fin + ((size_t)n * (W - 1) + r) * C + c0, f);
@@ -367,14 +367,14 @@ kda_short_conv_bwd_kernel(const T* __restrict__ x, const float* __restrict__ wei
 // tap per block, eight tile lanes.
 __global__ void __launch_bounds__(256)
 kda_short_conv_params_kernel(const float* __restrict__ part, float* __restrict__ grad_weight,
-                             float* __restrict__ grad_bias, int C, int W, long long tiles)
+                             float* __restrict__ grad_bias, int C, int W, int tiles)
 {
     __shared__ float red[8][33];
     const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane, j = blockIdx.y;
     float s = 0.f;
     if (c < C)
-        for (long long i = y; i < tiles; i += 8) s += part[((size_t)i * (W + 1) + j) * C + c];
+        for (int i = y; i < tiles; i += 8) s += part[((size_t)i * (W + 1) + j) * C + c];
     red[y][lane] = s;
     __syncthreads();
     if (y == 0 && c < C) {
@@ -436,7 +436,7 @@ Seqs seqs_of(const int32_t* cu, int B, int T, int N)
     s.cu = cu;
     s.N = N;
     s.T = T;
-    s.total = (long long)B * T;
+    s.total = B * T;
     return s;
 }
 
@@ -450,7 +450,7 @@ cudaError_t fwd(const ConvArgs& a, cudaStream_t stream)
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     kda_short_conv_kernel<T, W, V><<<(unsigned)blocks, dim3(s.tx, s.ty), 0, stream>>>(
         (const T*)a.x, a.weight, a.bias, (const T*)a.initial_state, (T*)a.out, (T*)a.final_state,
-        seqs_of(a.cu_seqlens, a.B, a.T, a.N), a.C, s.ncb, s.tiles, s.run, a.silu);
+        seqs_of(a.cu_seqlens, a.B, a.T, a.N), a.C, s.ncb, (int)s.tiles, s.run, a.silu);
     return cudaGetLastError();
 }
 
@@ -477,11 +477,11 @@ cudaError_t bwd(const ConvArgs& a, cudaStream_t stream)
         kda_short_conv_bwd_kernel<T, W, V><<<(unsigned)blocks, dim3(s.tx, s.ty), smem, stream>>>(
             (const T*)a.x, a.weight, a.bias, (const T*)a.initial_state, (const T*)a.d_out, a.d_final_state,
             a.grad_x, a.grad_initial_state, (float*)a.workspace, seqs_of(a.cu_seqlens, a.B, a.T, a.N), a.C, s.ncb,
-            s.tiles, s.run, a.silu);
+            (int)s.tiles, s.run, a.silu);
         if (cudaError_t e = cudaGetLastError()) return e;
     }
     kda_short_conv_params_kernel<<<dim3((a.C + 31) / 32, W + (a.grad_bias ? 1 : 0)), 256, 0, stream>>>(
-        (const float*)a.workspace, a.grad_weight, a.grad_bias, a.C, W, s.tiles);
+        (const float*)a.workspace, a.grad_weight, a.grad_bias, a.C, W, (int)s.tiles);
     return cudaGetLastError();
 }
 

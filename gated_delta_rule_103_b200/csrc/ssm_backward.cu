@@ -52,12 +52,12 @@ template <typename T, typename Tl, bool kY>
 struct Feed {
     ChannelRows<T, Tl> u, d, z, o;
     StateRows<T, Tl, kY> bc;
-    __device__ __forceinline__ void fetch(const BwdParams<T>& p, long long t, long long end, int c0, int nch, int g,
+    __device__ __forceinline__ void fetch(const BwdParams<T>& p, int t, int end, int c0, int nch, int g,
                                           int tid)
     {
         const int q4 = (tid % Tl::Q) * 4, nq = nch - q4, D = p.f.D;
         const size_t at = (size_t)(t + tid / Tl::Q) * D + c0 + q4;
-        const int left = (end - t < Tl::TT ? (int)(end - t) : Tl::TT) - tid / Tl::Q;
+        const int left = (end - t < Tl::TT ? end - t : Tl::TT) - tid / Tl::Q;
         u.load(p.f.u, at, D, left, nq, p.f.vec_d, tid);
         d.load(p.f.delta, at, D, left, nq, p.f.vec_d, tid);
         if (kY) {
@@ -66,7 +66,7 @@ struct Feed {
         }
         bc.load(p.f, t, end, g, tid);
     }
-    __device__ __forceinline__ void stage(const BwdParams<T>& p, long long t, long long end, const float (&bias)[4],
+    __device__ __forceinline__ void stage(const BwdParams<T>& p, int t, int end, const float (&bias)[4],
                                           Elem* s, float* sB, float* sC, float* dt_sum, int tid)
     {
         const int q4 = (tid % Tl::Q) * 4;
@@ -112,12 +112,12 @@ kda_ssm_bwd_carry_kernel(BwdParams<T> p)
     float* s_C = s_B + 2 * TT * SP;                                 // [2][TT][SP]
     const int tid = threadIdx.x;
     const int across = p.f.G * p.f.cpb;
-    const long long slot = blockIdx.x / across;
+    const int slot = blockIdx.x / across;
     const int gb = (int)(blockIdx.x % across), g = gb / p.f.cpb;
-    int n, seg;
-    long long t0, end;
-    if (!p.f.units.locate(slot, n, seg, t0, end)) return;
-    if (p.f.units.count(n) == 1) return;
+    int n, seg, t0, end;
+    bool last;
+    if (!p.f.units.locate(slot, n, seg, last, t0, end)) return;
+    if (seg == 0 && last) return;
     const int cg = (gb % p.f.cpb) * CH;
     const int nch = p.f.Dg - cg < CH ? p.f.Dg - cg : CH;
     const int c0 = g * p.f.Dg + cg;
@@ -140,7 +140,7 @@ kda_ssm_bwd_carry_kernel(BwdParams<T> p)
     if (t0 + TT < end) feed.fetch(p, t0 + TT, end, c0, nch, g, tid);
     __syncthreads();
     int buf = 0;
-    for (long long t = t0; t < end; t += TT, buf ^= 1) {
+    for (int t = t0; t < end; t += TT, buf ^= 1) {
         if (t + TT < end) {
             const int nb = buf ^ 1;
             feed.stage(p, t + TT, end, bias, s_e + nb * TT * CH, s_B + nb * TT * SP, s_C + nb * TT * SP, dt_sum, tid);
@@ -194,7 +194,7 @@ kda_ssm_bwd_chain_kernel(const float* __restrict__ A, const float* __restrict__ 
     const size_t i = (size_t)(blockIdx.x % per) * 256 + threadIdx.x;
     if (i >= DS) return;
     const float a = A[i] * kLog2e;
-    const long long first = units.first(n);
+    const int first = units.first(n);
     const int cnt = units.count(n);
     float c = d_fin ? d_fin[(size_t)n * DS + i] : 0.f;
     float* e = exits + (size_t)first * DS + i;
@@ -245,7 +245,7 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int D = p.f.D, S = p.f.S;
     const int across = p.f.G * p.f.cpb;
-    const long long slot = blockIdx.x / across;
+    const int slot = blockIdx.x / across;
     const int gb = (int)(blockIdx.x % across), g = gb / p.f.cpb;
     const int cg = (gb % p.f.cpb) * CH;
     const int nch = p.f.Dg - cg < CH ? p.f.Dg - cg : CH;
@@ -254,9 +254,9 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
     const bool chan = ch < nch;
     const size_t row = (size_t)(c0 + (chan ? ch : 0)) * S;
     const size_t DS = (size_t)D * S;
-    int n, seg;
-    long long t0, end;
-    if (!p.f.units.locate(slot, n, seg, t0, end)) {
+    int n, seg, t0, end;
+    bool last;
+    if (!p.f.units.locate(slot, n, seg, last, t0, end)) {
         // an empty slot adds nothing to the parameters' gradients
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -264,10 +264,8 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
         if (tid < nch) p.part_d[(size_t)slot * 2 * D + c0 + tid] = p.part_d[((size_t)slot * 2 + 1) * D + c0 + tid] = 0.f;
         return;
     }
-    const bool last = seg + 1 == p.f.units.count(n);
     // tiles of all units, numbered so that no count of earlier ones is needed
-    const long long tile0 = t0 / TT + slot;
-    const int tiles = (int)((end - t0 + TT - 1) / TT);
+    const int tile0 = t0 / TT + slot, tiles = (end - t0 + TT - 1) / TT;
 
     float A[4], h[4], c[4], bias[4], skip[4];
     const int q4 = (tid % Q) * 4;
@@ -308,7 +306,7 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
         __syncthreads();
         int buf = 0;
         for (int k = 0; k < tiles; ++k, buf ^= 1) {
-            const long long t = t0 + (long long)k * TT;
+            const int t = t0 + k * TT;
             if (t + TT < end) {
                 const int nb = buf ^ 1;
                 feed.stage(p, t + TT, end, bias, s_e + nb * TT * CH, s_B + nb * TT * SP, s_C, nullptr, tid);
@@ -329,9 +327,9 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
     // backward, from the last tile (its entry state is in h) to the first
     Feed<T, Tl, true> feed;
     float sum_skip[4] = {0.f, 0.f, 0.f, 0.f}, sum_bias[4] = {0.f, 0.f, 0.f, 0.f};
-    if (tiles > 0) feed.fetch(p, t0 + (long long)(tiles - 1) * TT, end, c0, nch, g, tid);
+    if (tiles > 0) feed.fetch(p, t0 + (tiles - 1) * TT, end, c0, nch, g, tid);
     for (int k = tiles - 1; k >= 0; --k) {
-        const long long t = t0 + (long long)k * TT;
+        const int t = t0 + k * TT;
         feed.stage(p, t, end, bias, s_e, s_B, s_C, nullptr, tid);
         __syncthreads();
         // The tile goes by in fours: their entry states first (each thread's own
@@ -519,7 +517,7 @@ __global__ void __launch_bounds__(256)
 kda_ssm_bwd_bc_kernel(const float* __restrict__ part, float* __restrict__ grad_B, float* __restrict__ grad_C,
                       Seqs seqs, int G, int S, int cpb)
 {
-    const long long all = seqs.total * G * 2 * S;
+    const long long all = (long long)seqs.total * G * 2 * S;
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
     if (i >= all) return;
     const long long row = i / (2 * S), t = row / G;

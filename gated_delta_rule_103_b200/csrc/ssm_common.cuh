@@ -207,9 +207,9 @@ struct StateRows {
     // whole rounds of the threads over B, then C: which is which is known at compile time
     static constexpr bool kRounds = ONE % Tl::THREADS == 0 && Tl::THREADS % SQ == 0;
     Raw4<T> r[NB];
-    __device__ __forceinline__ void load(const Params<T>& p, long long t0, long long end, int g, int tid)
+    __device__ __forceinline__ void load(const Params<T>& p, int t0, int end, int g, int tid)
     {
-        const int left = end - t0 < TT ? (int)(end - t0) : TT;
+        const int left = end - t0 < TT ? end - t0 : TT;
         const int s = (tid % SQ) * 4;
         if constexpr (kRounds) {
             constexpr int PER = ONE / Tl::THREADS, STEP = Tl::THREADS / SQ;
@@ -287,7 +287,7 @@ inline Units units_of(const int32_t* cu, int B, int T, int N, int len)
     u.s.cu = cu;
     u.s.N = N;
     u.s.T = T;
-    u.s.total = (long long)B * T;
+    u.s.total = B * T;
     u.len = len;
     u.per_seq = T > 0 ? (T + len - 1) / len : 1;
     return u;

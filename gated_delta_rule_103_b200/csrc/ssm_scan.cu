@@ -50,12 +50,11 @@ kda_ssm_scan_kernel(Params<T> p)
 
     const int lane = threadIdx.x & 31;
     const int across = p.G * p.cpb;
-    const long long slot = blockIdx.x / across;
+    const int slot = blockIdx.x / across;
     const int gb = (int)(blockIdx.x % across), g = gb / p.cpb;
-    int n, seg;
-    long long t0, end;
-    if (!p.units.locate(slot, n, seg, t0, end)) return;
-    const bool last = seg + 1 == p.units.count(n);
+    int n, seg, t0, end;
+    bool last;
+    if (!p.units.locate(slot, n, seg, last, t0, end)) return;
     if (kCarry && last) return;
     const int cg = (gb % p.cpb) * CH;                      // first channel within the group
     const int nch = p.Dg - cg < CH ? p.Dg - cg : CH;       // channels of this block
@@ -101,7 +100,7 @@ kda_ssm_scan_kernel(Params<T> p)
     StateRows<T, Tl, !kCarry> bc;
     // the tile from token t on (tokens behind the end repeat the last)
     const size_t step = (size_t)TB * p.D;
-    auto fetch = [&](long long t) {
+    auto fetch = [&](int t) {
         if (t + TT <= end) {
             size_t at = (size_t)(t + tok) * p.D;
 #pragma unroll
@@ -115,7 +114,7 @@ kda_ssm_scan_kernel(Params<T> p)
         } else {
 #pragma unroll
             for (int e = 0; e < NB; ++e) {
-                const long long tt = t + e * TB + tok;
+                const int tt = t + e * TB + tok;
                 const size_t at = (size_t)(tt < end ? tt : end - 1) * p.D;
 #pragma unroll
                 for (int o = 0; o < OWN; ++o) {
@@ -129,8 +128,8 @@ kda_ssm_scan_kernel(Params<T> p)
     };
 
     if (t0 < end) fetch(t0);
-    for (long long t = t0; t < end; t += TT) {
-        const int left = end - t < TT ? (int)(end - t) : TT;
+    for (int t = t0; t < end; t += TT) {
+        const int left = end - t < TT ? end - t : TT;
         float x[NB][OWN], zz[NB][OWN], dt[NB * OWN];
 #pragma unroll
         for (int e = 0; e < NB; ++e)
@@ -259,7 +258,7 @@ kda_ssm_chain_kernel(const float* __restrict__ A, const float* __restrict__ init
     if (i >= DS) return;
     const float a = A[i] * kLog2e;
     const size_t d = i / S;
-    const long long first = units.first(n);
+    const int first = units.first(n);
     const int cnt = units.count(n);
     float h = init ? init[(size_t)n * DS + i] : 0.f;
     float* e = ends + (size_t)first * DS + i;
@@ -287,7 +286,7 @@ kda_ssm_chain_kernel(const float* __restrict__ A, const float* __restrict__ init
 // states: whole rows of states go by in 16-byte accesses.  A thread takes its
 // channel of R sequences, whose states are in flight together and share A.
 template <typename T, int L, bool kVec, int R>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 3)
 kda_ssm_step_kernel(const T* __restrict__ u, const T* __restrict__ delta, const float* __restrict__ A,
                     const T* __restrict__ Bm, const T* __restrict__ Cm, const float* __restrict__ skip,
                     const T* __restrict__ z, const float* __restrict__ delta_bias, float* state,
@@ -299,7 +298,6 @@ kda_ssm_step_kernel(const T* __restrict__ u, const T* __restrict__ delta, const 
     const bool live = at < D;
     const int d = live ? at : 0;
     const int g = d / Dg;
-    float h[R][4], a[4], B[R][4], C[R][4], x[R][1], dv[R][1], zz[R][1];
     auto row4 = [&](const auto* p, float(&v)[4]) {
         if constexpr (kVec) {
             if (s0 < S) {
@@ -314,45 +312,65 @@ kda_ssm_step_kernel(const T* __restrict__ u, const T* __restrict__ delta, const 
             v[i] = w[0];
         }
     };
+    // every state first: each is read once and written once (streaming accesses)
+    float4 h[R];
+    T x[R], dv[R], zz[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int n = n0 + r < N ? n0 + r : N - 1;
-        row4(state + ((size_t)n * D + d) * S + s0, h[r]);
+        const float* st = state + ((size_t)n * D + d) * S + s0;
+        if (kVec && s0 < S) {
+            h[r] = __ldcs(reinterpret_cast<const float4*>(st));
+        } else {
+            float v[4];
+            row4(st, v);
+            h[r] = make_float4(v[0], v[1], v[2], v[3]);
+        }
     }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const size_t nd = (size_t)(n0 + r < N ? n0 + r : N - 1) * D + d;
+        x[r] = u[nd];
+        dv[r] = delta[nd];
+        if (z) zz[r] = z[nd];
+    }
+    float a[4];
     row4(A + (size_t)d * S + s0, a);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int n = n0 + r < N ? n0 + r : N - 1;
-        const size_t bc = ((size_t)n * G + g) * S + s0, nd = (size_t)n * D + d;
-        row4(Bm + bc, B[r]);
-        row4(Cm + bc, C[r]);
-        load_vec<1>(u + nd, x[r]);
-        load_vec<1>(delta + nd, dv[r]);
-        zz[r][0] = 0.f;
-        if (z) load_vec<1>(z + nd, zz[r]);
-    }
     const float bias = delta_bias ? delta_bias[d] : 0.f, sk = skip ? skip[d] : 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] *= kLog2e;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int n = n0 + r;
-        float dt = dv[r][0] + bias;
+        const size_t bc = ((size_t)(n < N ? n : N - 1) * G + g) * S + s0;
+        float B[4], C[4], xx[1], dd[1];
+        row4(Bm + bc, B);
+        row4(Cm + bc, C);
+        load_vec<1>(&x[r], xx);
+        load_vec<1>(&dv[r], dd);
+        float dt = dd[0] + bias;
         if (use_softplus) dt = softplus(dt);
-        const float du = dt * x[r][0];
-        float y = 0.f;
+        const float du = dt * xx[0];
+        float hh[4] = {h[r].x, h[r].y, h[r].z, h[r].w}, y = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            h[r][i] = fmaf(ex2(dt * a[i]), h[r][i], du * B[r][i]);
-            y = fmaf(h[r][i], C[r][i], y);
+            hh[i] = fmaf(ex2(dt * a[i]), hh[i], du * B[i]);
+            y = fmaf(hh[i], C[i], y);
         }
         const bool here = live && n < N;
-        if (here) store4(state + ((size_t)n * D + d) * S + s0, h[r], kVec && s0 < S, S - s0);
+        if (here) {
+            float* st = state + ((size_t)n * D + d) * S + s0;
+            if (kVec && s0 < S) __stcs(reinterpret_cast<float4*>(st), make_float4(hh[0], hh[1], hh[2], hh[3]));
+            else store4(st, hh, false, S - s0);
+        }
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
         if (here && l == 0) {
-            y = fmaf(sk, x[r][0], y);
-            if (z) y *= silu(zz[r][0]);
+            y = fmaf(sk, xx[0], y);
+            if (z) {
+                load_vec<1>(&zz[r], xx);
+                y *= silu(xx[0]);
+            }
             const float o[1] = {y};
             store_vec<1>(out + (size_t)n * D + d, o);
         }
@@ -379,8 +397,8 @@ cudaError_t fwd(const ScanArgs& a, cudaStream_t st)
 {
     const Cut c = fwd_cut(a.B, a.T, a.D, a.S, a.N, a.cu_seqlens != nullptr);
     Params<T> p = params_of<T>(a, c.len, Fwd<L>::CH);
-    const long long slots = p.units.slots();
-    const long long blocks = slots * p.G * p.cpb;
+    const int slots = p.units.slots();
+    const long long blocks = (long long)slots * p.G * p.cpb;
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (blocks == 0) return cudaSuccess;
     if (c.cut) {
@@ -398,13 +416,13 @@ template <typename T, int L>
 cudaError_t step(const ScanArgs& a, cudaStream_t st)
 {
     const int across = (int)(((long long)a.D * L + 255) / 256);
-    // four sequences a thread once that still fills every SM's threads
-    const int R = (long long)across * a.N >= 4LL * 8 * sm_count() ? 4 : 1;
+    // eight sequences a thread once that still fills every SM three times
+    const int R = (long long)across * a.N >= 8LL * 3 * sm_count() ? 8 : 1;
     const long long blocks = (long long)across * ((a.N + R - 1) / R);
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (blocks == 0) return cudaSuccess;
     const bool vec = a.S % 4 == 0;
-    auto* k = R == 4 ? (vec ? &kda_ssm_step_kernel<T, L, true, 4> : &kda_ssm_step_kernel<T, L, false, 4>)
+    auto* k = R == 8 ? (vec ? &kda_ssm_step_kernel<T, L, true, 8> : &kda_ssm_step_kernel<T, L, false, 8>)
                      : (vec ? &kda_ssm_step_kernel<T, L, true, 1> : &kda_ssm_step_kernel<T, L, false, 1>);
     k<<<(unsigned)blocks, 256, 0, st>>>((const T*)a.u, (const T*)a.delta, a.A, (const T*)a.Bm, (const T*)a.Cm, a.skip,
                                         (const T*)a.z, a.delta_bias, a.final_state, (T*)a.out, a.N, a.D, a.S,

@@ -374,7 +374,7 @@ size_t kda_chunk_bwd_workspace_bytes(int B, int T, int H, int N, int packed, kda
  *    that belong to no sequence are neither read nor written (per token,
  *    kda_group_norm_* takes every row and does not read cu_seqlens).
  *    Sequences may be empty.
- *  - B * T up to 2^31 - 1, channels up to 2^24; more: KDA_ERR_UNSUPPORTED.
+ *  - B * T and N up to 2^30, channels up to 2^24; more: KDA_ERR_UNSUPPORTED.
  *  - No output may overlap another tensor of the call, except that
  *    final_state may be the same pointer as initial_state.
  *  - Results do not depend on what else runs: sums are taken in a fixed order.
