@@ -41,150 +41,159 @@ __device__ __forceinline__ float part_sum(float v, int lanes)
 
 // ---- per token --------------------------------------------------------------
 // LANES lanes hold one row of Cg = C / G values, NV vectors of V each (lane l:
-// values (l + i LANES) V).  A lane keeps to one group, so that its weights
-// stay in registers while it walks the tokens.
-template <typename T, int V, int LANES, int NV, bool kBwd>
-__global__ void __launch_bounds__(256)
+// values (l + i LANES) V; kFull: they are Cg to the last one).  A lane keeps to
+// one group, so that its weights stay in registers while it walks the tokens, U
+// at a time: their loads are in flight and their sums are folded together.
+constexpr int rows_blocks(int nv, bool full, bool bwd)  // per SM
+{
+    return bwd ? (nv == 1 ? 2 : 1) : (nv == 1 ? (full ? 4 : 3) : 2);
+}
+
+template <typename T, int V, int LANES, int NV, bool kFull, bool kBwd>
+__global__ void __launch_bounds__(256, rows_blocks(NV, kFull, kBwd))
 kda_norm_rows_kernel(const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
                      T* __restrict__ out, float* __restrict__ mean, float* __restrict__ rstd,
                      const T* __restrict__ d_out, float* __restrict__ grad_x, float* __restrict__ part,
-                     long long rows, int G, int Cg, int walkers, float eps, int act)
+                     int rows, int G, int Cg, int walkers, float eps, int act)
 {
     // walker k of group g takes rows k, k + walkers, ...
     const long long id = ((long long)blockIdx.x * 256 + threadIdx.x) / LANES;
     const int lane = threadIdx.x & (LANES - 1);
-    const int g = (int)(id % G);
-    const long long k = id / G;
-    const bool live = k < walkers;  // a whole row's lanes agree; the warp stays together for the sums
-    float w[NV][V], b[NV][V], dw[NV][V], db[NV][V];
+    const int g = (int)(id % G), k = (int)(id / G);
+    const bool live = k < walkers;  // a row's lanes agree; the warp stays together for the sums
+    auto in = [&](int i) { return kFull || (lane + i * LANES) * V < Cg; };
+    const size_t col = (size_t)g * Cg + lane * V, C = (size_t)G * Cg;
+    float w[NV][V], b[NV][V];
+    float dw[kBwd ? NV : 1][V], db[kBwd ? NV : 1][V];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (lane + i * LANES) * V;
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            w[i][j] = c < Cg && weight ? weight[(size_t)g * Cg + c + j] : 1.f;
-            b[i][j] = c < Cg && bias ? bias[(size_t)g * Cg + c + j] : 0.f;
-            dw[i][j] = db[i][j] = 0.f;
+            w[i][j] = in(i) && weight ? weight[col + i * LANES * V + j] : 1.f;
+            b[i][j] = in(i) && bias ? bias[col + i * LANES * V + j] : 0.f;
+            if (kBwd) dw[kBwd ? i : 0][j] = db[kBwd ? i : 0][j] = 0.f;
         }
-    }
     const float inv = 1.f / (float)Cg;
-    constexpr int U = kBwd ? (NV == 1 ? 2 : 1) : 4 / NV;  // rows in flight per lane
-    const long long steps = (rows + walkers - 1) / walkers;
-    for (long long s = 0; s < steps; s += U) {
+    constexpr int U = NV == 1 ? 2 : 1;
+    const int steps = (rows + walkers - 1) / walkers;
+    for (int s = 0; s < steps; s += U) {
+        size_t at[U];
+        bool here[U];
         Raw<T, V> rx[U][NV], rd[kBwd ? U : 1][kBwd ? NV : 1];
-        float ms[U], rss[U];
+        float m[U], rs[U];
 #pragma unroll
         for (int q = 0; q < U; ++q) {
-            const long long r = k + (s + q) * walkers;
-            const bool here = live && r < rows;
-            const size_t at = ((size_t)r * G + g) * Cg;
+            const int r = live && s + q < steps ? k + (s + q) * walkers : rows;
+            here[q] = r < rows;
+            at[q] = (size_t)(here[q] ? r : rows - 1) * C + col;  // a row behind the last repeats it
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (lane + i * LANES) * V;
-                if (here && c < Cg) {
-                    rx[q][i].load(x + at + c);
-                    if constexpr (kBwd) rd[q][i].load(d_out + at + c);
+            for (int i = 0; i < NV; ++i)
+                if (in(i)) {
+                    rx[q][i].load(x + at[q] + i * LANES * V);
+                    if constexpr (kBwd) rd[q][i].load(d_out + at[q] + i * LANES * V);
                 }
-            }
             if (kBwd) {
-                ms[q] = here ? mean[(size_t)r * G + g] : 0.f;
-                rss[q] = here ? rstd[(size_t)r * G + g] : 0.f;
+                m[q] = mean[(size_t)(here[q] ? r : rows - 1) * G + g];
+                rs[q] = rstd[(size_t)(here[q] ? r : rows - 1) * G + g];
             }
         }
+        float v[U][NV][V], s1[U], s2[U];
 #pragma unroll
         for (int q = 0; q < U; ++q) {
-            const long long r = k + (s + q) * walkers;
-            const bool here = live && r < rows;
-            const size_t at = ((size_t)r * G + g) * Cg;
-            float v[NV][V];
+            s1[q] = s2[q] = 0.f;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = (lane + i * LANES) * V;
-                if (here && c < Cg) rx[q][i].get(v[i]);
+                if (in(i)) rx[q][i].get(v[q][i]);
                 else
 #pragma unroll
-                    for (int j = 0; j < V; ++j) v[i][j] = 0.f;
+                    for (int j = 0; j < V; ++j) v[q][i][j] = 0.f;
             }
-            if constexpr (!kBwd) {
-                float sum = 0.f;
+        }
+        if constexpr (!kBwd) {
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
-                    for (int j = 0; j < V; ++j) sum += v[i][j];
-                const float m = lane_sum<LANES>(sum) * inv;
-                float sq = 0.f;
+                    for (int j = 0; j < V; ++j) s1[q] += v[q][i][j];
+                m[q] = lane_sum<LANES>(s1[q]) * inv;
+            }
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (in(i))
+#pragma unroll
+                        for (int j = 0; j < V; ++j) {
+                            const float d = v[q][i][j] - m[q];
+                            s2[q] = fmaf(d, d, s2[q]);
+                        }
+                rs[q] = 1.f / sqrtf(fmaf(lane_sum<LANES>(s2[q]), inv, eps));
+            }
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+                if (!here[q]) continue;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int c = (lane + i * LANES) * V;
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        const float d = c < Cg ? v[i][j] - m : 0.f;
-                        sq = fmaf(d, d, sq);
-                    }
-                }
-                const float rs = 1.f / sqrtf(fmaf(lane_sum<LANES>(sq), inv, eps));
-                if (!here) continue;
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int c = (lane + i * LANES) * V;
-                    if (c >= Cg) continue;
+                    if (!in(i)) continue;
                     float y[V];
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
-                        y[j] = fmaf((v[i][j] - m) * rs, w[i][j], b[i][j]);
+                        y[j] = fmaf((v[q][i][j] - m[q]) * rs[q], w[i][j], b[i][j]);
                         if (act) y[j] = silu(y[j]);
                     }
-                    store_vec<V>(out + at + c, y);
+                    store_vec<V>(out + at[q] + i * LANES * V, y);
                 }
                 if (lane == 0) {
-                    mean[(size_t)r * G + g] = m;
-                    rstd[(size_t)r * G + g] = rs;
+                    const size_t r = (size_t)(k + (s + q) * walkers) * G + g;
+                    mean[r] = m[q];
+                    rstd[r] = rs[q];
                 }
-            } else {
-                const float m = ms[q], rs = rss[q];
-                float dy[NV][V], s1 = 0.f, s2 = 0.f;
+            }
+        } else {
+            float dy[U][NV][V];
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int c = (lane + i * LANES) * V;
-                    if (here && c < Cg) rd[q][i].get(dy[i]);
-                    else
-#pragma unroll
-                        for (int j = 0; j < V; ++j) dy[i][j] = 0.f;
+                    if (in(i)) rd[q][i].get(dy[q][i]);
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
-                        v[i][j] = (v[i][j] - m) * rs;  // xhat
-                        if (act) dy[i][j] *= silu_slope(fmaf(v[i][j], w[i][j], b[i][j]));
-                        if (!here || c >= Cg) v[i][j] = dy[i][j] = 0.f;
-                        dw[i][j] = fmaf(dy[i][j], v[i][j], dw[i][j]);
-                        db[i][j] += dy[i][j];
-                        dy[i][j] *= w[i][j];
-                        s1 += dy[i][j];
-                        s2 = fmaf(dy[i][j], v[i][j], s2);
+                        float& d = dy[q][i][j];
+                        if (!in(i)) d = 0.f;
+                        const float xh = v[q][i][j] = (v[q][i][j] - m[q]) * rs[q];
+                        if (act) d *= silu_slope(fmaf(xh, w[i][j], b[i][j]));
+                        if (!here[q]) d = 0.f;
+                        dw[i][j] = fmaf(d, xh, dw[i][j]);
+                        db[i][j] += d;
+                        d *= w[i][j];
+                        s1[q] += d;
+                        s2[q] = fmaf(d, xh, s2[q]);
                     }
                 }
-                s1 = lane_sum<LANES>(s1) * inv;
-                s2 = lane_sum<LANES>(s2) * inv;
-                if (!here) continue;
+                s1[q] = lane_sum<LANES>(s1[q]) * inv;
+                s2[q] = lane_sum<LANES>(s2[q]) * inv;
+            }
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+                if (!here[q]) continue;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int c = (lane + i * LANES) * V;
-                    if (c >= Cg) continue;
+                    if (!in(i)) continue;
                     float dx[V];
 #pragma unroll
-                    for (int j = 0; j < V; ++j) dx[j] = rs * (dy[i][j] - s1 - v[i][j] * s2);
-                    store_vec<V>(grad_x + at + c, dx);
+                    for (int j = 0; j < V; ++j) dx[j] = rs[q] * (dy[q][i][j] - s1[q] - v[q][i][j] * s2[q]);
+                    store_vec<V>(grad_x + at[q] + i * LANES * V, dx);
                 }
             }
         }
     }
     if (kBwd && live) {
-        const size_t C = (size_t)G * Cg;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (lane + i * LANES) * V;
-            if (c >= Cg) continue;
-            store_vec<V>(part + ((size_t)k * 2) * C + (size_t)g * Cg + c, dw[i]);
-            store_vec<V>(part + ((size_t)k * 2 + 1) * C + (size_t)g * Cg + c, db[i]);
+            if (!in(i)) continue;
+            store_vec<V>(part + ((size_t)k * 2) * C + col + i * LANES * V, dw[kBwd ? i : 0]);
+            store_vec<V>(part + ((size_t)k * 2 + 1) * C + col + i * LANES * V, db[kBwd ? i : 0]);
         }
     }
 }
@@ -382,10 +391,10 @@ kda_norm_stats_kernel(const T* __restrict__ x, float* __restrict__ part, Units u
     sm[threadIdx.x] = mean;
     sq[threadIdx.x] = dev;
     __syncthreads();
-    // over a group's threads: `lg` lanes a group
+    // over a group's threads, `lg` lanes a group: all groups at once where they fit
     const int per = wide ? 256 : l.cpg * l.ty;
     int lg = 32;
-    while (lg > 1 && lg / 2 >= per) lg >>= 1;
+    while (lg > 1 && (lg / 2 >= per || lg * groups > l.threads)) lg >>= 1;
     const int sub = threadIdx.x % lg, across = l.threads / lg;
     const float inv = 1.f / ((float)(b - a) * (float)(l.cpg * V));
     for (int g1 = 0; g1 < groups; g1 += across) {
@@ -508,7 +517,8 @@ kda_norm_bwd_sums_kernel(const T* __restrict__ x, const float* __restrict__ weig
                          const T* __restrict__ d_out, float* __restrict__ part, float* __restrict__ gsum,
                          Units units, Layout l, int C, int G, int act)
 {
-    __shared__ float red[2 * V * 256];  // per thread, then [2][channels] of the block
+    __shared__ float red[2 * V * 256];  // per thread, then per column of the block
+    __shared__ float red_g[2][256];     // per thread: sums of k and k xhat
     int n, seg, a, b;
     bool last;
     const int unit = blockIdx.x / l.ngb;
@@ -559,6 +569,8 @@ kda_norm_bwd_sums_kernel(const T* __restrict__ x, const float* __restrict__ weig
             for (int j = 0; j < V; ++j) {
                 red[j * 256 + threadIdx.x] = dw[j];
                 red[(V + j) * 256 + threadIdx.x] = db[j];
+                s1 = fmaf(w[j], db[j], s1);
+                s2 = fmaf(w[j], dw[j], s2);
             }
         }
     }
@@ -571,32 +583,29 @@ kda_norm_bwd_sums_kernel(const T* __restrict__ x, const float* __restrict__ weig
         }
         return;
     }
+    red_g[0][threadIdx.x] = s1;
+    red_g[1][threadIdx.x] = s2;
     __syncthreads();
-    // a column's token lanes, into its first one's place
-    for (int q = threadIdx.x; q < 2 * V * l.cols; q += l.threads) {
-        const int which = q / l.cols, c = q - which * l.cols;
-        float s = 0.f;
-        for (int y = 0; y < l.ty; ++y) s += red[which * 256 + y * l.cols + c];
-        red[which * 256 + c] = s;
+    // over a column's token lanes, and over a group's threads
+    for (int q = threadIdx.x; q < 2 * chans; q += l.threads) {
+        const int which = q >= chans, c = q - which * chans;
+        const float* r = red + (which * V + c % V) * 256 + c / V;
+        float t = 0.f;
+        for (int y = 0; y < l.ty; ++y) t += r[y * l.cols];
+        (which ? pb : pw)[c] = t;
     }
-    __syncthreads();
-    for (int c = threadIdx.x; c < chans; c += l.threads) {
-        pw[c] = red[(c % V) * 256 + c / V];
-        pb[c] = red[(V + c % V) * 256 + c / V];
-    }
-    const int per = l.cpg * V;
+    const int per = l.cpg * l.ty;
     int lg = 32;
-    while (lg > 1 && lg / 2 >= per) lg >>= 1;
+    while (lg > 1 && (lg / 2 >= per || lg * groups > l.threads)) lg >>= 1;
     const int sub = threadIdx.x % lg;
     for (int g1 = 0; g1 < groups; g1 += l.threads / lg) {
         const int g = g1 + threadIdx.x / lg;
         float t1 = 0.f, t2 = 0.f;
         if (g < groups)
             for (int i = sub; i < per; i += lg) {
-                const int c = g * per + i;
-                const float w = weight ? weight[ch0 + c] : 1.f;
-                t1 = fmaf(w, red[(V + c % V) * 256 + c / V], t1);
-                t2 = fmaf(w, red[(c % V) * 256 + c / V], t2);
+                const int at = (i / l.cpg) * l.cols + g * l.cpg + i % l.cpg;
+                t1 += red_g[0][at];
+                t2 += red_g[1][at];
             }
         t1 = part_sum(t1, lg);
         t2 = part_sum(t2, lg);
@@ -723,8 +732,8 @@ RowShape row_shape(long long rows, int C, int G, kda_dtype dtype, bool bwd)
     while (r.nv * r.lanes < vecs) r.nv <<= 1;
     const int per_block = r.nv <= 4 ? 256 / r.lanes : 1;  // rows in flight
     if (r.nv > 4) r.lanes = r.nv = 0;
-    // enough walkers for every SM's warps, none without a row
-    const long long want = (long long)sm_count() * (bwd ? 4 : 8) * per_block;
+    // as many walkers as the SMs hold at a time, none without a row
+    const long long want = (long long)sm_count() * (r.nv ? rows_blocks(r.nv, r.lanes * r.nv * r.V == Cg, bwd) : 4) * per_block;
     long long w = (want + G - 1) / G;
     if (w > rows) w = rows;
     if (w < 1) w = 1;
@@ -736,11 +745,17 @@ RowShape row_shape(long long rows, int C, int G, kda_dtype dtype, bool bwd)
 template <typename T, int V, int LANES, bool kBwd>
 cudaError_t rows_nv(const NormArgs& a, const RowShape& r, cudaStream_t st)
 {
-    const long long rows = (long long)a.B * a.T;
-#define KDA_NORM_ROWS(NV)                                                                                      \
-    kda_norm_rows_kernel<T, V, LANES, NV, kBwd><<<(unsigned)r.blocks, 256, 0, st>>>(                           \
+    const int rows = a.B * a.T;
+    const bool full = r.lanes * r.nv * V == a.C / a.G;
+#define KDA_NORM_ROWS_OF(NV, FULL)                                                                             \
+    kda_norm_rows_kernel<T, V, LANES, NV, FULL, kBwd><<<(unsigned)r.blocks, 256, 0, st>>>(                     \
         (const T*)a.x, a.weight, a.bias, (T*)a.out, a.mean, a.rstd, (const T*)a.d_out, a.grad_x,               \
         (float*)a.workspace, rows, a.G, a.C / a.G, r.walkers, a.eps, a.silu)
+#define KDA_NORM_ROWS(NV)                                                                                      \
+    do {                                                                                                       \
+        if (full) KDA_NORM_ROWS_OF(NV, true);                                                                  \
+        else KDA_NORM_ROWS_OF(NV, false);                                                                      \
+    } while (0)
     if constexpr (LANES < 32) {
         KDA_NORM_ROWS(1);
     } else {
@@ -749,6 +764,7 @@ cudaError_t rows_nv(const NormArgs& a, const RowShape& r, cudaStream_t st)
         else KDA_NORM_ROWS(4);
     }
 #undef KDA_NORM_ROWS
+#undef KDA_NORM_ROWS_OF
     return cudaGetLastError();
 }
 

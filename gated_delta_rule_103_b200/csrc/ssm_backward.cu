@@ -7,12 +7,13 @@
 //     dA   = sum_t g_t a_t h_{t-1} dt
 //     dz   = d_out y silu'(z)         d delta = d dt softplus'(delta + bias)
 //
-// A block walks its unit forward once, leaving the state at every tile's entry
-// in the workspace, then backward tile by tile: the tile's states are computed
-// again into registers and used up from its last token to its first.  Sums
-// over a channel's lanes and over a warp's channels are folded (ssm_common.cuh),
-// the warps' in shared memory, the blocks' and units' by kernels in a fixed
-// order, so that results do not change from run to run.
+// The state at every tile's entry is written to the workspace first (a forward
+// walk, ssm_scan.cu); then a block goes through its unit's tiles from the last
+// to the first: a tile's states are computed again, four tokens at a time held in
+// registers, and used up from the last token to the first.  Sums over a
+// channel's lanes and over a warp's channels are folded (ssm_common.cuh), the
+// warps' in shared memory, the blocks' and units' by kernels in a fixed order,
+// so that results do not change from run to run.
 //
 // Where sequences are cut into units, a pass before it gives every unit its
 // end state from zero, its sum of dt, and the adjoint it hands to the unit in
@@ -24,10 +25,10 @@ namespace {
 
 using namespace ssm;
 
-constexpr int kThreads = 256;
-
-template <int L>
-using BTile = Tile<L, 4, (L == 4 || L == 8) ? 16 : 8, kThreads>;
+template <int LANES>
+using Carry = Shape<LANES, 4, 32>;
+template <int LANES>
+using Bwd = Shape<LANES, 4, 128>;
 
 template <typename T>
 struct BwdParams {
@@ -36,149 +37,155 @@ struct BwdParams {
     const float* d_fin;
     float *gu, *gdelta, *gz, *ginit;
     float* exits;    // per slot [D][S]: adjoint handed to the unit in front, then the one from behind
-    float* entries;  // per tile [D][S]: state at the tile's entry
     float* part_bc;  // [cpb][tokens][G][2][S]
     float* part_A;   // per slot [D][S]
     float* part_d;   // per slot [2][D]: skip, delta_bias
 };
 
-// What both passes do to a tile's (token, channel) operands: dt, dt u and dy
-// as fp32 in shared memory.
-struct Elem {
-    float dt, du, dy, pad;
+// This lane's elements of a tile, raw: tokens TB e + tok of its channels.
+template <typename T, typename Sh>
+struct Elements {
+    T u[Sh::NB][Sh::OWN], d[Sh::NB][Sh::OWN], z[Sh::NB][Sh::OWN], o[Sh::NB][Sh::OWN];
+    // tokens behind the end repeat the last
+    __device__ __forceinline__ void fetch(const BwdParams<T>& p, int t, int end, const int (&own)[Sh::OWN])
+    {
+#pragma unroll
+        for (int e = 0; e < Sh::NB; ++e) {
+            const int tt = t + e * Sh::TB;
+            const size_t at = (size_t)(tt < end ? tt : end - 1) * p.f.D;
+#pragma unroll
+            for (int i = 0; i < Sh::OWN; ++i) {
+                u[e][i] = p.f.u[at + own[i]];
+                d[e][i] = p.f.delta[at + own[i]];
+                o[e][i] = p.d_out[at + own[i]];
+                if (p.f.z) z[e][i] = p.f.z[at + own[i]];
+            }
+        }
+    }
 };
 
-template <typename T, typename Tl, bool kY>
-struct Feed {
-    ChannelRows<T, Tl> u, d, z, o;
-    StateRows<T, Tl, kY> bc;
-    __device__ __forceinline__ void fetch(const BwdParams<T>& p, int t, int end, int c0, int nch, int g,
-                                          int tid)
+template <typename T>
+__device__ __forceinline__ float one(const T& v)
+{
+    float x[1];
+    load_vec<1>(&v, x);
+    return x[0];
+}
+
+// A block's place: its unit and channels.
+struct Place {
+    int slot, g, gb, c0, nch, n, seg, t0, end;
+    bool last, found;
+    template <typename T>
+    __device__ __forceinline__ Place(const Params<T>& p, int CH)
     {
-        const int q4 = (tid % Tl::Q) * 4, nq = nch - q4, D = p.f.D;
-        const size_t at = (size_t)(t + tid / Tl::Q) * D + c0 + q4;
-        const int left = (end - t < Tl::TT ? end - t : Tl::TT) - tid / Tl::Q;
-        u.load(p.f.u, at, D, left, nq, p.f.vec_d, tid);
-        d.load(p.f.delta, at, D, left, nq, p.f.vec_d, tid);
-        if (kY) {
-            if (p.f.z) z.load(p.f.z, at, D, left, nq, p.f.vec_d, tid);
-            o.load(p.d_out, at, D, left, nq, p.f.vec_d, tid);
-        }
-        bc.load(p.f, t, end, g, tid);
-    }
-    __device__ __forceinline__ void stage(const BwdParams<T>& p, int t, int end, const float (&bias)[4],
-                                          Elem* s, float* sB, float* sC, float* dt_sum, int tid)
-    {
-        const int q4 = (tid % Tl::Q) * 4;
-#pragma unroll
-        for (int k = 0; k < Tl::IPT; ++k) {
-            const int tt = (tid + k * kThreads) / Tl::Q;
-            if (tt >= Tl::TT) break;
-            float x[4], dv[4], dy[4] = {0.f, 0.f, 0.f, 0.f}, zz[4];
-            u.r[k].get(x);
-            d.r[k].get(dv);
-            if (kY) {
-                o.r[k].get(dy);
-                if (p.f.z) {
-                    z.r[k].get(zz);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) dy[i] *= silu(zz[i]);
-                }
-            }
-            const bool in = t + tt < end;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float v = dv[i] + bias[i];
-                if (p.f.softplus) v = softplus(v);
-                if (!in) v = 0.f;
-                if (dt_sum) dt_sum[i] += v;
-                *reinterpret_cast<float4*>(&s[tt * Tl::CH + q4 + i]) = make_float4(v, v * x[i], dy[i], 0.f);
-            }
-        }
-        bc.put(sB, sC, tid);
+        const int across = p.G * p.cpb;
+        slot = blockIdx.x / across;
+        gb = (int)(blockIdx.x % across);
+        g = gb / p.cpb;
+        gb -= g * p.cpb;
+        nch = p.Dg - gb * CH < CH ? p.Dg - gb * CH : CH;
+        c0 = g * p.Dg + gb * CH;
+        found = p.units.locate(slot, n, seg, last, t0, end);
     }
 };
 
 // End state from zero, sum of dt and handed-on adjoint of every unit.
-template <typename T, int L>
-__global__ void __launch_bounds__(kThreads, 2)
+template <typename T, int LANES>
+__global__ void __launch_bounds__(32)
 kda_ssm_bwd_carry_kernel(BwdParams<T> p)
 {
-    using Tl = BTile<L>;
-    constexpr int CH = Tl::CH, TT = Tl::TT, SP = Tl::SP, Q = Tl::Q;
-    extern __shared__ __align__(16) unsigned char smem[];
-    Elem* s_e = reinterpret_cast<Elem*>(smem);                      // [2][TT][CH]
-    float* s_B = reinterpret_cast<float*>(s_e + 2 * TT * CH);       // [2][TT][SP]
-    float* s_C = s_B + 2 * TT * SP;                                 // [2][TT][SP]
-    const int tid = threadIdx.x;
-    const int across = p.f.G * p.f.cpb;
-    const int slot = blockIdx.x / across;
-    const int gb = (int)(blockIdx.x % across), g = gb / p.f.cpb;
-    int n, seg, t0, end;
-    bool last;
-    if (!p.f.units.locate(slot, n, seg, last, t0, end)) return;
-    if (seg == 0 && last) return;
-    const int cg = (gb % p.f.cpb) * CH;
-    const int nch = p.f.Dg - cg < CH ? p.f.Dg - cg : CH;
-    const int c0 = g * p.f.Dg + cg;
-    const int ch = tid / L, s0 = (tid % L) * 4;
-    const bool chan = ch < nch;
-    const size_t row = (size_t)(c0 + (chan ? ch : 0)) * p.f.S;
-    float A[4], bias[4], dt_sum[4];
-    const int q4 = (tid % Q) * 4;
+    using Sh = Carry<LANES>;
+    constexpr int L = Sh::L, TT = Sh::TT, SP = Sh::SP, TB = Sh::TB, NB = Sh::NB, OWN = Sh::OWN, PAIRS = Sh::PAIRS;
+    __shared__ __align__(16) float2 s_dt[TT][PAIRS][2];  // dt, dt u
+    __shared__ __align__(16) float s_dy[TT][PAIRS][2];
+    __shared__ __align__(16) float s_B[TT * SP], s_C[TT * SP];
+    const Place at(p.f, Sh::CH);
+    if (!at.found || (at.seg == 0 && at.last)) return;
+    const int lane = threadIdx.x & 31, pair = lane / L, s0 = lane % L * 4;
+    float A[2][4], h[2][4], P[2][4], R[2][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        A[i] = chan && s0 + i < p.f.S ? p.f.A[row + s0 + i] * kLog2e : 0.f;
-        dt_sum[i] = 0.f;
-        bias[i] = p.f.delta_bias && q4 + i < nch ? p.f.delta_bias[c0 + q4 + i] : 0.f;
-    }
-    const float2 A01 = make_float2(A[0], A[1]), A23 = make_float2(A[2], A[3]);
-    float2 h01 = both(0.f), h23 = h01, R01 = h01, R23 = h01, P01 = both(1.f), P23 = P01;
-    Feed<T, Tl, true> feed;
-    feed.fetch(p, t0, end, c0, nch, g, tid);
-    feed.stage(p, t0, end, bias, s_e, s_B, s_C, dt_sum, tid);
-    if (t0 + TT < end) feed.fetch(p, t0 + TT, end, c0, nch, g, tid);
-    __syncthreads();
-    int buf = 0;
-    for (int t = t0; t < end; t += TT, buf ^= 1) {
-        if (t + TT < end) {
-            const int nb = buf ^ 1;
-            feed.stage(p, t + TT, end, bias, s_e + nb * TT * CH, s_B + nb * TT * SP, s_C + nb * TT * SP, dt_sum, tid);
-            if (t + 2 * TT < end) feed.fetch(p, t + 2 * TT, end, c0, nch, g, tid);
-        }
-#pragma unroll 4
-        for (int j = 0; j < TT; ++j) {
-            const float4 e = *reinterpret_cast<const float4*>(&s_e[(buf * TT + j) * CH + ch]);
-            const float4 B = *reinterpret_cast<const float4*>(&s_B[(buf * TT + j) * SP + s0]);
-            const float4 C = *reinterpret_cast<const float4*>(&s_C[(buf * TT + j) * SP + s0]);
-            const float2 dt = both(e.x), du = both(e.y), dy = both(e.z);
-            const float2 a01 = ex2(mul2(dt, A01)), a23 = ex2(mul2(dt, A23));
-            h01 = fma2(a01, h01, mul2(du, make_float2(B.x, B.y)));
-            h23 = fma2(a23, h23, mul2(du, make_float2(B.z, B.w)));
-            P01 = mul2(P01, a01);
-            P23 = mul2(P23, a23);
-            R01 = fma2(P01, mul2(dy, make_float2(C.x, C.y)), R01);
-            R23 = fma2(P23, mul2(dy, make_float2(C.z, C.w)), R23);
-        }
-        __syncthreads();
-    }
-    const float h[4] = {h01.x, h01.y, h23.x, h23.y}, R[4] = {R01.x, R01.y, R23.x, R23.y};
+    for (int r = 0; r < 2; ++r) {
+        const int c = pair * 2 + r < at.nch ? pair * 2 + r : at.nch - 1;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (chan && s0 + i < p.f.S) {
-            p.f.ends[(size_t)slot * p.f.D * p.f.S + row + s0 + i] = h[i];
-            p.exits[(size_t)slot * p.f.D * p.f.S + row + s0 + i] = R[i];
+        for (int i = 0; i < 4; ++i) {
+            A[r][i] = s0 + i < p.f.S ? p.f.A[(size_t)(at.c0 + c) * p.f.S + s0 + i] * kLog2e : 0.f;
+            h[r][i] = R[r][i] = 0.f;
+            P[r][i] = 1.f;
         }
-    float* red = reinterpret_cast<float*>(smem);
-    if (tid / Q < TT) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) red[(tid / Q) * CH + q4 + i] = dt_sum[i];
     }
-    __syncthreads();
-    if (tid < nch) {
-        float s = 0.f;
-        for (int r = 0; r < Tl::ROWS; ++r) s += red[r * CH + tid];
-        p.f.steps[(size_t)slot * p.f.D + c0 + tid] = s;
+    const int tok = fold_index<Sh::BITS>(lane, 2);
+    const bool owner = L == 1 || lane % L < 2 * TB;
+    int own[OWN];
+    float bias[OWN], dt_sum[OWN];
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+        const int c = pair * 2 + (OWN == 2 ? o : lane & 1);
+        own[o] = at.c0 + (c < at.nch ? c : at.nch - 1);
+        bias[o] = p.f.delta_bias ? p.f.delta_bias[own[o]] : 0.f;
+        dt_sum[o] = 0.f;
+    }
+    Elements<T, Sh> el;
+    StateRows<T, Sh, true> bc;
+    el.fetch(p, at.t0 + tok, at.end, own);
+    bc.load(p.f, at.t0, at.end, at.g, lane);
+    for (int t = at.t0; t < at.end; t += TT) {
+#pragma unroll
+        for (int e = 0; e < NB; ++e)
+#pragma unroll
+            for (int o = 0; o < OWN; ++o) {
+                const int tt = e * TB + tok, c = OWN == 2 ? o : lane & 1;
+                float dt = one(el.d[e][o]) + bias[o];
+                if (p.f.softplus) dt = softplus(dt);
+                if (t + tt >= at.end) dt = 0.f;  // a step of nothing
+                float dy = t + tt < at.end ? one(el.o[e][o]) : 0.f;
+                if (p.f.z) dy *= silu(one(el.z[e][o]));
+                if (owner) {
+                    dt_sum[o] += dt;
+                    s_dt[tt][pair][c] = make_float2(dt, dt * one(el.u[e][o]));
+                    s_dy[tt][pair][c] = t + tt < at.end ? dy : 0.f;
+                }
+            }
+        bc.put(s_B, s_C, lane);
+        if (t + TT < at.end) {
+            el.fetch(p, t + TT + tok, at.end, own);
+            bc.load(p.f, t + TT, at.end, at.g, lane);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) {
+            const float4 dd = *reinterpret_cast<const float4*>(&s_dt[tt][pair][0]);
+            const float2 dy = *reinterpret_cast<const float2*>(&s_dy[tt][pair][0]);
+            const float4 B4 = *reinterpret_cast<const float4*>(&s_B[tt * SP + s0]);
+            const float4 C4 = *reinterpret_cast<const float4*>(&s_C[tt * SP + s0]);
+            const float B[4] = {B4.x, B4.y, B4.z, B4.w}, C[4] = {C4.x, C4.y, C4.z, C4.w};
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float a = ex2((r ? dd.z : dd.x) * A[r][i]);
+                    h[r][i] = fmaf(a, h[r][i], (r ? dd.w : dd.y) * B[i]);
+                    P[r][i] *= a;
+                    R[r][i] = fmaf(P[r][i], (r ? dy.y : dy.x) * C[i], R[r][i]);
+                }
+        }
+        __syncwarp();
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+        if (pair * 2 + r < at.nch) {
+            const size_t row = ((size_t)at.slot * p.f.D + at.c0 + pair * 2 + r) * p.f.S + s0;
+            const bool whole = p.f.vec_s && s0 < p.f.S;
+            store4(p.f.ends + row, h[r], whole, p.f.S - s0);
+            store4(p.exits + row, R[r], whole, p.f.S - s0);
+        }
+    // a channel's tokens lie with the lanes of its parity
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+#pragma unroll
+        for (int i = 2; i < L; i <<= 1) dt_sum[o] += __shfl_xor_sync(0xffffffffu, dt_sum[o], i);
+        const int c = pair * 2 + (OWN == 2 ? o : lane & 1);
+        if (c < at.nch && lane % L < 2) p.f.steps[(size_t)at.slot * p.f.D + at.c0 + c] = dt_sum[o];
     }
 }
 
@@ -217,296 +224,277 @@ kda_ssm_bwd_chain_kernel(const float* __restrict__ A, const float* __restrict__ 
     }
 }
 
-template <typename T, int L>
-constexpr size_t bwd_smem()
-{
-    using Tl = BTile<L>;
-    // staged operands, results per (token, channel), warps' sums of dB and dC,
-    // entry states of every four tokens
-    return sizeof(float) * (2 * Tl::TT * Tl::CH * 4 + 4 * Tl::TT * Tl::SP + 3 * Tl::TT * (Tl::CH + 8) +
-                            (kThreads / 32) * Tl::TT * 2 * Tl::SP + Tl::TT * kThreads);
-}
+// Shared memory of the main kernel, in floats.
+template <typename Sh>
+struct BwdSpace {
+    static constexpr int kB = 0;                                            // [TT][SP]
+    static constexpr int kC = kB + Sh::TT * Sh::SP;                          // [TT][SP]
+    static constexpr int kDt = kC + Sh::TT * Sh::SP;                         // per warp [TT][PAIRS][2]: dt, dt u
+    static constexpr int kDy = kDt + Sh::WARPS * Sh::TT * Sh::PAIRS * 4;     // per warp [TT][PAIRS][2]
+    static constexpr int kEl = kDy + Sh::WARPS * Sh::TT * Sh::PAIRS * 2;     // per thread [NB OWN][4]: its elements
+    static constexpr int kM = kEl + Sh::THREADS * Sh::NB * Sh::OWN * 4;      // per thread [TT / 4][8]: states
+    static constexpr int kW = kM + Sh::THREADS * Sh::TT / 4 * 8;             // per warp [TT][2][SP]: dB, dC
+    static constexpr int kAll = kW + Sh::WARPS * Sh::TT * 2 * Sh::SP;
+};
 
-template <typename T, int L>
-__global__ void __launch_bounds__(kThreads, 2)
+template <typename T, int LANES>
+__global__ void __launch_bounds__(128, 2)
 kda_ssm_bwd_kernel(BwdParams<T> p)
 {
-    using Tl = BTile<L>;
-    constexpr int CH = Tl::CH, TT = Tl::TT, SP = Tl::SP, Q = Tl::Q, IPT = Tl::IPT;
-    constexpr int YP = CH + 8;  // no two of a warp's results in one bank
-    constexpr int WARPS = kThreads / 32, NL = 32 / L;               // channels of a warp
-    extern __shared__ __align__(16) unsigned char smem[];
-    Elem* s_e = reinterpret_cast<Elem*>(smem);                      // [2][TT][CH]
-    float* s_B = reinterpret_cast<float*>(s_e + 2 * TT * CH);       // [2][TT][SP]
-    float* s_C = s_B + 2 * TT * SP;                                 // [2][TT][SP]
-    float* s_o = s_C + 2 * TT * SP;                                 // [3][TT][YP]: g.B, sum g a h A, C.h
-    float* s_w = s_o + 3 * TT * YP;                                 // [WARPS][TT][2][SP]
-    float4* s_m = reinterpret_cast<float4*>(s_w + WARPS * TT * 2 * SP);  // [TT / 4][threads]
+    using Sh = Bwd<LANES>;
+    using Sp = BwdSpace<Sh>;
+    constexpr int L = Sh::L, TT = Sh::TT, SP = Sh::SP, TB = Sh::TB, NB = Sh::NB, OWN = Sh::OWN, PAIRS = Sh::PAIRS;
+    constexpr int THREADS = Sh::THREADS, WARPS = Sh::WARPS, BPG = 4 / TB;  // batches per four tokens
+    extern __shared__ __align__(16) float smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float* s_B = smem + Sp::kB;
+    float* s_C = smem + Sp::kC;
+    float4* s_dt = reinterpret_cast<float4*>(smem + Sp::kDt) + warp * TT * PAIRS;  // of a pair's two channels
+    float2* s_dy = reinterpret_cast<float2*>(smem + Sp::kDy) + warp * TT * PAIRS;
+    float4* s_el = reinterpret_cast<float4*>(smem + Sp::kEl) + tid;                // stride THREADS
+    float4* s_m = reinterpret_cast<float4*>(smem + Sp::kM) + tid;
+    float* s_w = smem + Sp::kW;
     const int D = p.f.D, S = p.f.S;
-    const int across = p.f.G * p.f.cpb;
-    const int slot = blockIdx.x / across;
-    const int gb = (int)(blockIdx.x % across), g = gb / p.f.cpb;
-    const int cg = (gb % p.f.cpb) * CH;
-    const int nch = p.f.Dg - cg < CH ? p.f.Dg - cg : CH;
-    const int c0 = g * p.f.Dg + cg;
-    const int ch = tid / L, s0 = (tid % L) * 4;
-    const bool chan = ch < nch;
-    const size_t row = (size_t)(c0 + (chan ? ch : 0)) * S;
     const size_t DS = (size_t)D * S;
-    int n, seg, t0, end;
-    bool last;
-    if (!p.f.units.locate(slot, n, seg, last, t0, end)) {
+    const Place at(p.f, Sh::CH);
+    const int pair = lane / L, s0 = lane % L * 4, ch0 = warp * Sh::WCH + pair * 2;  // the pair's first channel
+    const bool whole = p.f.vec_s && s0 < S;
+    if (!at.found) {
         // an empty slot adds nothing to the parameters' gradients
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (chan && s0 + i < S) p.part_A[(size_t)slot * DS + row + s0 + i] = 0.f;
-        if (tid < nch) p.part_d[(size_t)slot * 2 * D + c0 + tid] = p.part_d[((size_t)slot * 2 + 1) * D + c0 + tid] = 0.f;
+        for (int c = tid; c < at.nch; c += THREADS) {
+            for (int s = 0; s < S; ++s) p.part_A[(size_t)at.slot * DS + (size_t)(at.c0 + c) * S + s] = 0.f;
+            p.part_d[(size_t)at.slot * 2 * D + at.c0 + c] = p.part_d[((size_t)at.slot * 2 + 1) * D + at.c0 + c] = 0.f;
+        }
         return;
     }
     // tiles of all units, numbered so that no count of earlier ones is needed
-    const int tile0 = t0 / TT + slot, tiles = (end - t0 + TT - 1) / TT;
+    const int tile0 = at.t0 / TT + at.slot, tiles = (at.end - at.t0 + TT - 1) / TT;
 
-    float A[4], h[4], c[4], bias[4], skip[4];
-    const int q4 = (tid % Q) * 4;
+    float A[2][4], c[2][4], dA[2][4];
+    size_t row[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool ok = chan && s0 + i < S;
-        const size_t at = row + s0 + i;
-        A[i] = ok ? p.f.A[at] * kLog2e : 0.f;
-        h[i] = c[i] = 0.f;
-        if (ok) {
-            if (p.f.ends && seg > 0) h[i] = p.f.ends[(size_t)slot * DS + at];
-            else if (p.f.init) h[i] = p.f.init[(size_t)n * DS + at];
-            if (p.f.ends && !last) c[i] = p.exits[(size_t)slot * DS + at];
-            else if (p.d_fin) c[i] = p.d_fin[(size_t)n * DS + at];
+    for (int r = 0; r < 2; ++r) {
+        const int ch = ch0 + r < at.nch ? ch0 + r : at.nch - 1;
+        row[r] = (size_t)(at.c0 + ch) * S + s0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool ok = s0 + i < S;
+            A[r][i] = ok ? p.f.A[row[r] + i] * kLog2e : 0.f;
+            c[r][i] = dA[r][i] = 0.f;
+            if (ok) {
+                if (p.f.ends && !at.last) c[r][i] = p.exits[(size_t)at.slot * DS + row[r] + i];
+                else if (p.d_fin) c[r][i] = p.d_fin[(size_t)at.n * DS + row[r] + i];
+            }
         }
-        bias[i] = p.f.delta_bias && q4 + i < nch ? p.f.delta_bias[c0 + q4 + i] : 0.f;
-        skip[i] = p.f.skip && q4 + i < nch ? p.f.skip[c0 + q4 + i] : 0.f;
+    }
+    // this lane's elements
+    const int tok = fold_index<Sh::BITS>(lane, 2);
+    const bool owner = L == 1 || lane % L < 2 * TB;
+    int own[OWN];
+    float bias[OWN], skip[OWN], sum_skip[OWN], sum_bias[OWN];
+    bool mine[OWN];
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+        const int ch = ch0 + (OWN == 2 ? o : lane & 1);
+        mine[o] = owner && ch < at.nch;
+        own[o] = at.c0 + (ch < at.nch ? ch : at.nch - 1);
+        bias[o] = p.f.delta_bias ? p.f.delta_bias[own[o]] : 0.f;
+        skip[o] = p.f.skip ? p.f.skip[own[o]] : 0.f;
+        sum_skip[o] = sum_bias[o] = 0.f;
     }
 
-    const float2 A01 = make_float2(A[0], A[1]), A23 = make_float2(A[2], A[3]);
-    float2 h01 = make_float2(h[0], h[1]), h23 = make_float2(h[2], h[3]);
-    float2 c01 = make_float2(c[0], c[1]), c23 = make_float2(c[2], c[3]);
-    float2 dA01 = both(0.f), dA23 = dA01;
-    auto advance = [&](int j, float2& x01, float2& x23) {
-        const float2 dd = *reinterpret_cast<const float2*>(&s_e[j * CH + ch]);
-        const float4 B = *reinterpret_cast<const float4*>(&s_B[j * SP + s0]);
-        const float2 dt = both(dd.x), du = both(dd.y);
-        x01 = fma2(ex2(mul2(dt, A01)), x01, mul2(du, make_float2(B.x, B.y)));
-        x23 = fma2(ex2(mul2(dt, A23)), x23, mul2(du, make_float2(B.z, B.w)));
+    Elements<T, Sh> el;
+    StateRows<T, Sh, true> bc;
+    float h[2][4];
+    auto fetch = [&](int k) {
+        const int t = at.t0 + k * TT;
+        el.fetch(p, t + tok, at.end, own);
+        bc.load(p.f, t, at.end, at.g, tid);
+        const float* e = p.f.entries + (size_t)(tile0 + k) * DS;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            if (whole) {
+                load_vec<4>(e + row[r], h[r]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[r][i] = s0 + i < S ? e[row[r] + i] : 0.f;
+            }
+        }
+    };
+    auto advance = [&](int tt) {
+        const float4 dd = s_dt[tt * PAIRS + pair];
+        const float4 B4 = *reinterpret_cast<const float4*>(&s_B[tt * SP + s0]);
+        const float B[4] = {B4.x, B4.y, B4.z, B4.w};
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                h[r][i] = fmaf(ex2((r ? dd.z : dd.x) * A[r][i]), h[r][i], (r ? dd.w : dd.y) * B[i]);
     };
 
-    // forward: the state at every tile's entry
-    {
-        Feed<T, Tl, false> feed;
-        feed.fetch(p, t0, end, c0, nch, g, tid);
-        feed.stage(p, t0, end, bias, s_e, s_B, s_C, nullptr, tid);
-        if (t0 + TT < end) feed.fetch(p, t0 + TT, end, c0, nch, g, tid);
-        __syncthreads();
-        int buf = 0;
-        for (int k = 0; k < tiles; ++k, buf ^= 1) {
-            const int t = t0 + k * TT;
-            if (t + TT < end) {
-                const int nb = buf ^ 1;
-                feed.stage(p, t + TT, end, bias, s_e + nb * TT * CH, s_B + nb * TT * SP, s_C, nullptr, tid);
-                if (t + 2 * TT < end) feed.fetch(p, t + 2 * TT, end, c0, nch, g, tid);
-            }
-            float* e = p.entries + (size_t)(tile0 + k) * DS + row + s0;
-            if (chan) {
-                const float x[4] = {h01.x, h01.y, h23.x, h23.y};
-                store4(e, x, p.f.vec_s && s0 < S, S - s0);
-            }
-            if (k + 1 < tiles)
-#pragma unroll 4
-                for (int j = 0; j < TT; ++j) advance(buf * TT + j, h01, h23);
-            __syncthreads();
-        }
-    }
-
-    // backward, from the last tile (its entry state is in h) to the first
-    Feed<T, Tl, true> feed;
-    float sum_skip[4] = {0.f, 0.f, 0.f, 0.f}, sum_bias[4] = {0.f, 0.f, 0.f, 0.f};
-    if (tiles > 0) feed.fetch(p, t0 + (tiles - 1) * TT, end, c0, nch, g, tid);
+    if (tiles > 0) fetch(tiles - 1);
     for (int k = tiles - 1; k >= 0; --k) {
-        const int t = t0 + k * TT;
-        feed.stage(p, t, end, bias, s_e, s_B, s_C, nullptr, tid);
+        const int t = at.t0 + k * TT;
+        // what depends on (token, channel) alone
+#pragma unroll
+        for (int e = 0; e < NB; ++e)
+#pragma unroll
+            for (int o = 0; o < OWN; ++o) {
+                const int tt = e * TB + tok, ch = OWN == 2 ? o : lane & 1;
+                const bool in = t + tt < at.end && ch0 + ch < at.nch;  // others have no step and no adjoint
+                const float x = one(el.u[e][o]), raw = one(el.d[e][o]) + bias[o], dout = one(el.o[e][o]);
+                const float zz = p.f.z ? one(el.z[e][o]) : 0.f;
+                float dt = p.f.softplus ? softplus(raw) : raw;
+                if (!in) dt = 0.f;
+                const float dy = p.f.z ? dout * silu(zz) : dout;
+                if (owner) {
+                    reinterpret_cast<float2*>(s_dt)[(tt * PAIRS + pair) * 2 + ch] = make_float2(dt, dt * x);
+                    reinterpret_cast<float*>(s_dy)[(tt * PAIRS + pair) * 2 + ch] = in ? dy : 0.f;
+                    s_el[(e * OWN + o) * THREADS] = make_float4(x, dout, zz, raw);
+                }
+            }
+        bc.put(s_B, s_C, tid);
         __syncthreads();
-        // The tile goes by in fours: their entry states first (each thread's own
-        // in shared memory), then from the last four to the first their states
-        // and decays again, held in registers.
-#pragma unroll 1
+        // the states in front of every four tokens
+#pragma unroll
         for (int q = 0; q < TT / 4; ++q) {
-            s_m[q * kThreads + tid] = make_float4(h01.x, h01.y, h23.x, h23.y);
+            s_m[(2 * q) * THREADS] = make_float4(h[0][0], h[0][1], h[0][2], h[0][3]);
+            s_m[(2 * q + 1) * THREADS] = make_float4(h[1][0], h[1][1], h[1][2], h[1][3]);
             if (q + 1 < TT / 4)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) advance(q * 4 + j, h01, h23);
+                for (int j = 0; j < 4; ++j) advance(q * 4 + j);
         }
-        float2 dA01_t = both(0.f), dA23_t = dA01_t;
+        if (k > 0) fetch(k - 1);
+        // a tile's sum of dA first: long sums of small terms keep their digits
+        float dA_t[2][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dA_t[r][i] = 0.f;
 #pragma unroll 1
-        for (int tb = TT - 4; tb >= 0; tb -= 4) {
-            const float4 m = s_m[tb / 4 * kThreads + tid];
-            const float2 b01 = make_float2(m.x, m.y), b23 = make_float2(m.z, m.w);
-            float2 hs[4][2], as[4][2];
+        for (int q = TT / 4 - 1; q >= 0; --q) {
+            const float4 m0 = s_m[(2 * q) * THREADS], m1 = s_m[(2 * q + 1) * THREADS];
+            const float b[2][4] = {{m0.x, m0.y, m0.z, m0.w}, {m1.x, m1.y, m1.z, m1.w}};
+            float hs[4][2][4], as[4][2][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 dd = *reinterpret_cast<const float2*>(&s_e[(tb + j) * CH + ch]);
-                const float4 B = *reinterpret_cast<const float4*>(&s_B[(tb + j) * SP + s0]);
-                const float2 dt = both(dd.x), du = both(dd.y);
-                as[j][0] = ex2(mul2(dt, A01));
-                as[j][1] = ex2(mul2(dt, A23));
-                hs[j][0] = fma2(as[j][0], j ? hs[j > 0 ? j - 1 : 0][0] : b01, mul2(du, make_float2(B.x, B.y)));
-                hs[j][1] = fma2(as[j][1], j ? hs[j > 0 ? j - 1 : 0][1] : b23, mul2(du, make_float2(B.z, B.w)));
+                const float4 dd = s_dt[(q * 4 + j) * PAIRS + pair];
+                const float4 B4 = *reinterpret_cast<const float4*>(&s_B[(q * 4 + j) * SP + s0]);
+                const float B[4] = {B4.x, B4.y, B4.z, B4.w};
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        as[j][r][i] = ex2((r ? dd.z : dd.x) * A[r][i]);
+                        hs[j][r][i] = fmaf(as[j][r][i], j ? hs[j > 0 ? j - 1 : 0][r][i] : b[r][i], (r ? dd.w : dd.y) * B[i]);
+                    }
             }
-            float o[3][4];  // [what][token]
 #pragma unroll
-            for (int jj = 3; jj >= 0; --jj) {
-                const int tok = tb + jj;
-                const float4 e = *reinterpret_cast<const float4*>(&s_e[tok * CH + ch]);
-                const float4 B = *reinterpret_cast<const float4*>(&s_B[tok * SP + s0]);
-                const float4 C = *reinterpret_cast<const float4*>(&s_C[tok * SP + s0]);
-                const float2 dt = both(e.x), du = both(e.y), dy = both(e.z);
-                const float2 B01 = make_float2(B.x, B.y), B23 = make_float2(B.z, B.w);
-                const float2 C01 = make_float2(C.x, C.y), C23 = make_float2(C.z, C.w);
-                const float2 g01 = fma2(C01, dy, c01), g23 = fma2(C23, dy, c23);
-                c01 = mul2(as[jj][0], g01);
-                c23 = mul2(as[jj][1], g23);
-                const float2 w01 = mul2(c01, jj ? hs[jj > 0 ? jj - 1 : 0][0] : b01);
-                const float2 w23 = mul2(c23, jj ? hs[jj > 0 ? jj - 1 : 0][1] : b23);
-                dA01_t = fma2(w01, dt, dA01_t);
-                dA23_t = fma2(w23, dt, dA23_t);
-                const float2 gB = fma2(g01, B01, mul2(g23, B23));
-                const float2 wA = fma2(w01, A01, mul2(w23, A23));
-                const float2 hC = fma2(hs[jj][0], C01, mul2(hs[jj][1], C23));
-                o[0][jj] = gB.x + gB.y;
-                o[1][jj] = wA.x + wA.y;
-                o[2][jj] = hC.x + hC.y;
-                const float2 p0 = mul2(g01, du), p1 = mul2(g23, du);
-                const float2 p2 = mul2(hs[jj][0], dy), p3 = mul2(hs[jj][1], dy);
-                float bc[8] = {p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
-                fold<8, NL, L>(bc, lane);
-                constexpr int KEEP = NL >= 8 ? 1 : 8 / NL;
-                constexpr int BITS = NL >= 8 ? 3 : (NL == 4 ? 2 : (NL == 2 ? 1 : 0));
-                if (lane / L < 8) {
-                    const int at = fold_index<BITS>(lane, L) * KEEP;  // of {B: 0..3, C: 4..7}
+            for (int eb = BPG - 1; eb >= 0; --eb) {
+                float o[3][2 * TB];  // g . B, sum g a h A, C . h of [channel][token]
 #pragma unroll
-                    for (int i = 0; i < KEEP; ++i) {
-                        const int v = at + i;
-                        s_w[((warp * TT + tok) * 2 + (v >> 2)) * SP + s0 + (v & 3)] = bc[i];
+                for (int jj = TB - 1; jj >= 0; --jj) {
+                    const int j = eb * TB + jj, tt = q * 4 + j;
+                    const float4 dd = s_dt[tt * PAIRS + pair];
+                    const float2 dy2 = s_dy[tt * PAIRS + pair];
+                    const float4 B4 = *reinterpret_cast<const float4*>(&s_B[tt * SP + s0]);
+                    const float4 C4 = *reinterpret_cast<const float4*>(&s_C[tt * SP + s0]);
+                    const float B[4] = {B4.x, B4.y, B4.z, B4.w}, C[4] = {C4.x, C4.y, C4.z, C4.w};
+                    float bc8[8];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float dt = r ? dd.z : dd.x, du = r ? dd.w : dd.y, dy = r ? dy2.y : dy2.x;
+                        float gB = 0.f, wA = 0.f, hC = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float gg = fmaf(C[i], dy, c[r][i]);
+                            c[r][i] = as[j][r][i] * gg;
+                            const float w = c[r][i] * (j ? hs[j > 0 ? j - 1 : 0][r][i] : b[r][i]);
+                            dA_t[r][i] = fmaf(w, dt, dA_t[r][i]);
+                            gB = fmaf(gg, B[i], gB);
+                            wA = fmaf(w, A[r][i], wA);
+                            hC = fmaf(hs[j][r][i], C[i], hC);
+                            bc8[i] = r ? fmaf(gg, du, bc8[i]) : gg * du;
+                            bc8[4 + i] = r ? fmaf(hs[j][r][i], dy, bc8[4 + i]) : hs[j][r][i] * dy;
+                        }
+                        o[0][r * TB + jj] = gB;
+                        o[1][r * TB + jj] = wA;
+                        o[2][r * TB + jj] = hC;
+                    }
+                    // over the warp's pairs
+                    fold<8, PAIRS, L>(bc8, lane);
+                    constexpr int KEEP = PAIRS >= 8 ? 1 : 8 / PAIRS;
+                    constexpr int BITS = PAIRS >= 8 ? 3 : (PAIRS == 4 ? 2 : (PAIRS == 2 ? 1 : 0));
+                    if (PAIRS <= 8 || lane / L < 8) {
+                        const int first = fold_index<BITS>(lane, L) * KEEP;  // of {B: 0..3, C: 4..7}
+#pragma unroll
+                        for (int i = 0; i < KEEP; ++i) {
+                            const int v = first + i;
+                            s_w[((warp * TT + tt) * 2 + (v >> 2)) * SP + s0 + (v & 3)] = bc8[i];
+                        }
                     }
                 }
-            }
-            constexpr int KEEP = L >= 4 ? 1 : 4 / L;
-            constexpr int BITS = L >= 4 ? 2 : (L == 2 ? 1 : 0);
+                // over a pair's lanes, each left with its own element
+                fold<2 * TB, L, 1>(o[0], lane);
+                fold<2 * TB, L, 1>(o[1], lane);
+                if (p.f.z) fold<2 * TB, L, 1>(o[2], lane);
+                const int e = q * BPG + eb, tt = e * TB + tok;
 #pragma unroll
-            for (int w = 0; w < 3; ++w) {
-                if (w == 2 && !p.f.z) break;  // y is wanted for dz alone
-                fold<4, L, 1>(o[w], lane);
-                if (tid % L < 4) {
-                    const int at = tb + fold_index<BITS>(lane, 1) * KEEP;
-#pragma unroll
-                    for (int i = 0; i < KEEP; ++i) s_o[(w * TT + at + i) * YP + ch] = o[w][i];
+                for (int i = 0; i < OWN; ++i) {
+                    if (!mine[i] || t + tt >= at.end) continue;
+                    const float4 v = s_el[(e * OWN + i) * THREADS];  // u, d_out, z, delta + bias
+                    const float dt = reinterpret_cast<float2*>(s_dt)[(tt * PAIRS + pair) * 2 + (OWN == 2 ? i : lane & 1)].x;
+                    const size_t to = (size_t)(t + tt) * D + own[i];
+                    float dy = v.y;
+                    if (p.f.z) {
+                        const float sg = sigmoid(v.z);
+                        p.gz[to] = v.y * fmaf(skip[i], v.x, o[2][i]) * (sg * fmaf(v.z, 1.f - sg, 1.f));
+                        dy = v.y * v.z * sg;
+                    }
+                    p.gu[to] = fmaf(dt, o[0][i], skip[i] * dy);
+                    sum_skip[i] = fmaf(dy, v.x, sum_skip[i]);
+                    float gd = fmaf(v.x, o[0][i], o[1][i] * kLn2);
+                    if (p.f.softplus) gd *= sigmoid(v.w);
+                    sum_bias[i] += gd;
+                    p.gdelta[to] = gd;
                 }
             }
         }
-        // a tile's sum first: long sums of small terms keep their digits
-        dA01.x += dA01_t.x;
-        dA01.y += dA01_t.y;
-        dA23.x += dA23_t.x;
-        dA23.y += dA23_t.y;
-        if (k > 0) {
-            float next[4] = {0.f, 0.f, 0.f, 0.f};
-            const float* e = p.entries + (size_t)(tile0 + k - 1) * DS + row + s0;
-            if (chan) {
-                if (p.f.vec_s) {
-                    if (s0 < S) load_vec<4>(e, next);
-                } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (s0 + i < S) next[i] = e[i];
-                }
-            }
-            h01 = make_float2(next[0], next[1]);
-            h23 = make_float2(next[2], next[3]);
-        }
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dA[r][i] += dA_t[r][i];
         __syncthreads();
-        // gradients per (token, channel)
-#pragma unroll
-        for (int k2 = 0; k2 < IPT; ++k2) {
-            const int tt = (tid + k2 * kThreads) / Q;
-            if (tt >= TT || t + tt >= end || q4 >= nch) continue;
-            float x[4], dl[4], zz[4], dout[4], gb4[4], sa[4], y[4], r[4];
-            feed.u.r[k2].get(x);
-            feed.d.r[k2].get(dl);
-            feed.o.r[k2].get(dout);
-            load_vec<4>(&s_o[(0 * TT + tt) * YP + q4], gb4);
-            load_vec<4>(&s_o[(1 * TT + tt) * YP + q4], sa);
-            const size_t at = (size_t)(t + tt) * D + c0 + q4;
-            if (p.f.z) {
-                feed.z.r[k2].get(zz);
-                load_vec<4>(&s_o[(2 * TT + tt) * YP + q4], y);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float sg = sigmoid(zz[i]);
-                    r[i] = dout[i] * fmaf(skip[i], x[i], y[i]) * (sg * fmaf(zz[i], 1.f - sg, 1.f));
-                    dout[i] *= zz[i] * sg;
-                }
-                store4(p.gz + at, r, p.f.vec_d, nch - q4);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float dt = s_e[tt * CH + q4 + i].dt;
-                r[i] = fmaf(dt, gb4[i], skip[i] * dout[i]);
-                sum_skip[i] = fmaf(dout[i], x[i], sum_skip[i]);
-            }
-            store4(p.gu + at, r, p.f.vec_d, nch - q4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                r[i] = fmaf(x[i], gb4[i], sa[i] * kLn2);
-                if (p.f.softplus) r[i] *= sigmoid(dl[i] + bias[i]);
-                sum_bias[i] += r[i];
-            }
-            store4(p.gdelta + at, r, p.f.vec_d, nch - q4);
-        }
-        if (k > 0) feed.fetch(p, t - TT, end, c0, nch, g, tid);
         // dB and dC of this block's channels
-        for (int q = tid; q < TT * 2 * SP; q += kThreads) {
+        for (int q = tid; q < TT * 2 * SP; q += THREADS) {
             const int j = q / (2 * SP), ws = q - j * 2 * SP, s = ws % SP;
-            if (t + j >= end || s >= S) continue;
+            if (t + j >= at.end || s >= S) continue;
             float sum = 0.f;
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) sum += s_w[w * TT * 2 * SP + q];
-            p.part_bc[((((size_t)(gb % p.f.cpb) * p.f.units.s.total + t + j) * p.f.G + g) * 2 + ws / SP) * S + s] = sum;
+            p.part_bc[((((size_t)at.gb * p.f.units.s.total + t + j) * p.f.G + at.g) * 2 + ws / SP) * S + s] = sum;
         }
-        __syncthreads();
     }
 
-    if (chan) {
-        const float dA[4] = {dA01.x, dA01.y, dA23.x, dA23.y}, c_in[4] = {c01.x, c01.y, c23.x, c23.y};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (s0 + i < S) {
-                p.part_A[(size_t)slot * DS + row + s0 + i] = dA[i];
-                if (seg == 0 && p.ginit) p.ginit[(size_t)n * DS + row + s0 + i] = c_in[i];
-            }
-    }
-    float* red = reinterpret_cast<float*>(smem);
-    if (tid / Q < TT) {
+    for (int r = 0; r < 2; ++r)
+        if (ch0 + r < at.nch) {
+            store4(p.part_A + (size_t)at.slot * DS + row[r], dA[r], whole, S - s0);
+            if (at.seg == 0 && p.ginit) store4(p.ginit + (size_t)at.n * DS + row[r], c[r], whole, S - s0);
+        }
+    // a channel's tokens lie with the lanes of its parity
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            red[(tid / Q) * CH + q4 + i] = sum_skip[i];
-            red[(Tl::ROWS + tid / Q) * CH + q4 + i] = sum_bias[i];
+    for (int o = 0; o < OWN; ++o) {
+#pragma unroll
+        for (int i = 2; i < L; i <<= 1) {
+            sum_skip[o] += __shfl_xor_sync(0xffffffffu, sum_skip[o], i);
+            sum_bias[o] += __shfl_xor_sync(0xffffffffu, sum_bias[o], i);
         }
-    }
-    __syncthreads();
-    if (tid < nch) {
-        float a = 0.f, b = 0.f;
-        for (int r = 0; r < Tl::ROWS; ++r) {
-            a += red[r * CH + tid];
-            b += red[(Tl::ROWS + r) * CH + tid];
+        const int ch = ch0 + (OWN == 2 ? o : lane & 1);
+        if (ch < at.nch && lane % L < 2) {
+            p.part_d[(size_t)at.slot * 2 * D + at.c0 + ch] = sum_skip[o];
+            p.part_d[((size_t)at.slot * 2 + 1) * D + at.c0 + ch] = sum_bias[o];
         }
-        p.part_d[(size_t)slot * 2 * D + c0 + tid] = a;
-        p.part_d[((size_t)slot * 2 + 1) * D + c0 + tid] = b;
     }
 }
 
@@ -561,31 +549,23 @@ kda_ssm_bwd_params_kernel(const float* __restrict__ part_A, const float* __restr
     }
 }
 
-// Another walk over the unit's tokens is a fifth of the whole.
-constexpr int kBwdFewWarps = 12, kBwdWantWarps = 12, kBwdShortest = 64;
+// Sequences are cut where the chains give the SMs fewer warps than this: two
+// more walks then go over most tokens, a third of the whole.
+constexpr int kBwdFewWarps = 5, kBwdWantWarps = 8, kBwdShortest = 64;
 
 struct Layout {
     Cut c;
     size_t slots, tiles, ends, exits, steps, entries, bc, A, d, total;
 };
 
-// Lanes that share a channel.
-int bwd_lanes(int S)
-{
-    int l = 1;
-    while (4 * l < S) l <<= 1;
-    return l;
-}
-int bwd_tile_tokens(int L) { return L == 4 || L == 8 ? 16 : 8; }
-
 Layout layout_of(int B, int T, int D, int S, int G, int N, int packed)
 {
     Layout l = {};
-    const size_t tokens = (size_t)B * T, DS = (size_t)D * S, L = bwd_lanes(S);
-    l.c = cut_of(B, T, N, packed, (double)D * L / 32.0, kBwdFewWarps, kBwdWantWarps, kBwdShortest);
+    const size_t tokens = (size_t)B * T, DS = (size_t)D * S, L = lanes_of(S);
+    l.c = cut_of(B, T, N, packed, (double)D * L / 64.0, kBwdFewWarps, kBwdWantWarps, kBwdShortest);
     l.slots = (size_t)slots_of(B, T, N, packed, l.c.len);
-    const size_t CH = kThreads / L, cpb = ((size_t)(D / G) + CH - 1) / CH;
-    l.tiles = tokens / bwd_tile_tokens((int)L) + l.slots + 1;
+    const size_t CH = 256 / L, cpb = ((size_t)(D / G) + CH - 1) / CH, TT = L >= 4 ? 16 : 4 * L;  // as in Bwd<L>
+    l.tiles = tokens / TT + l.slots + 1;
     size_t at = 0;
     auto take = [&](size_t floats) {
         const size_t here = at;
@@ -604,12 +584,13 @@ Layout layout_of(int B, int T, int D, int S, int G, int N, int packed)
 }
 
 template <typename T, int L>
-cudaError_t bwd(const ScanArgs& a, cudaStream_t st)
+cudaError_t bwd(const ScanArgs& a, kda_dtype dtype, cudaStream_t st)
 {
+    static_assert(Bwd<L>::CH == 256 / L && Bwd<L>::TT == Shape<L, 16, 32>::TT, "workspace layout");
     const Layout l = layout_of(a.B, a.T, a.D, a.S, a.G, a.N, a.cu_seqlens != nullptr);
     char* ws = (char*)a.workspace;
     BwdParams<T> p = {};
-    p.f = params_of<T>(a, l.c.len, BTile<L>::CH);
+    p.f = params_of<T>(a, l.c.len, Bwd<L>::CH);
     p.d_out = (const T*)a.d_out;
     p.d_fin = a.d_final_state;
     p.gu = a.grad_u;
@@ -621,7 +602,7 @@ cudaError_t bwd(const ScanArgs& a, cudaStream_t st)
         p.exits = (float*)(ws + l.exits);
         p.f.steps = (float*)(ws + l.steps);
     }
-    p.entries = (float*)(ws + l.entries);
+    p.f.entries = (float*)(ws + l.entries);
     p.part_bc = (float*)(ws + l.bc);
     p.part_A = (float*)(ws + l.A);
     p.part_d = (float*)(ws + l.d);
@@ -629,17 +610,17 @@ cudaError_t bwd(const ScanArgs& a, cudaStream_t st)
     const long long chain = ((long long)a.D * a.S + 255) / 256 * a.N;
     const long long bc = ((long long)a.B * a.T * a.G * 2 * a.S + 255) / 256;
     if (blocks > INT32_MAX || chain > INT32_MAX || bc > INT32_MAX) return cudaErrorInvalidConfiguration;
-    constexpr size_t carry_smem = sizeof(float) * (2 * BTile<L>::TT * BTile<L>::CH * 4 + 4 * BTile<L>::TT * BTile<L>::SP);
-    constexpr size_t smem = bwd_smem<T, L>();
+    constexpr size_t smem = sizeof(float) * BwdSpace<Bwd<L>>::kAll;
     if (cudaError_t e = cudaFuncSetAttribute(kda_ssm_bwd_kernel<T, L>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)smem))
         return e;
     if (blocks > 0) {
         if (l.c.cut) {
-            if (cudaError_t e = cudaFuncSetAttribute(kda_ssm_bwd_carry_kernel<T, L>,
-                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)carry_smem))
-                return e;
-            kda_ssm_bwd_carry_kernel<T, L><<<(unsigned)blocks, kThreads, carry_smem, st>>>(p);
+            BwdParams<T> q = p;
+            q.f.cpb = (q.f.Dg + Carry<L>::CH - 1) / Carry<L>::CH;
+            const long long carry = (long long)l.slots * q.f.G * q.f.cpb;
+            if (carry > INT32_MAX) return cudaErrorInvalidConfiguration;
+            kda_ssm_bwd_carry_kernel<T, L><<<(unsigned)carry, 32, 0, st>>>(q);
             if (cudaError_t e = cudaGetLastError()) return e;
             if (cudaError_t e = launch_ssm_chain(a.A, a.initial_state, p.f.ends, p.f.steps, p.f.units, a.D, a.S, st))
                 return e;
@@ -647,7 +628,8 @@ cudaError_t bwd(const ScanArgs& a, cudaStream_t st)
                                                                      p.f.units, a.D, a.S);
             if (cudaError_t e = cudaGetLastError()) return e;
         }
-        kda_ssm_bwd_kernel<T, L><<<(unsigned)blocks, kThreads, smem, st>>>(p);
+        if (cudaError_t e = launch_ssm_entries(a, l.c.len, p.f.ends, p.f.entries, dtype, st)) return e;
+        kda_ssm_bwd_kernel<T, L><<<(unsigned)blocks, Bwd<L>::THREADS, smem, st>>>(p);
         if (cudaError_t e = cudaGetLastError()) return e;
     }
     if (bc > 0) {
@@ -661,15 +643,15 @@ cudaError_t bwd(const ScanArgs& a, cudaStream_t st)
 }
 
 template <typename T>
-cudaError_t by_states(const ScanArgs& a, cudaStream_t st)
+cudaError_t by_states(const ScanArgs& a, kda_dtype dtype, cudaStream_t st)
 {
-    switch (bwd_lanes(a.S)) {
-        case 1: return bwd<T, 1>(a, st);
-        case 2: return bwd<T, 2>(a, st);
-        case 4: return bwd<T, 4>(a, st);
-        case 8: return bwd<T, 8>(a, st);
-        case 16: return bwd<T, 16>(a, st);
-        case 32: return bwd<T, 32>(a, st);
+    switch (lanes_of(a.S)) {
+        case 1: return bwd<T, 1>(a, dtype, st);
+        case 2: return bwd<T, 2>(a, dtype, st);
+        case 4: return bwd<T, 4>(a, dtype, st);
+        case 8: return bwd<T, 8>(a, dtype, st);
+        case 16: return bwd<T, 16>(a, dtype, st);
+        case 32: return bwd<T, 32>(a, dtype, st);
     }
     return cudaErrorInvalidValue;
 }
@@ -683,7 +665,7 @@ size_t scan_bwd_workspace(int B, int T, int D, int S, int G, int N, int packed, 
 
 cudaError_t launch_scan_bwd(const ScanArgs& a, kda_dtype dtype, cudaStream_t st)
 {
-    return dtype == KDA_DTYPE_BF16 ? by_states<__nv_bfloat16>(a, st) : by_states<float>(a, st);
+    return dtype == KDA_DTYPE_BF16 ? by_states<__nv_bfloat16>(a, dtype, st) : by_states<float>(a, dtype, st);
 }
 
 }  // namespace kda

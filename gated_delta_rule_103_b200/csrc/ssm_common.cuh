@@ -4,11 +4,7 @@
 //     h[d, s] = a h[d, s] + dt u B[g, s];     y = sum_s h C[g, s] + skip u
 //     out = y, or y silu(z)
 //
-// Thread layout of every pass over tokens: a block takes THREADS / L channels
-// of one group; L neighbouring lanes share a channel and hold K states each (S
-// <= K L; states behind S have A = B = C = 0).  Tokens go by in tiles: what
-// depends on (token, channel) alone is computed once per element and handed to
-// the L lanes through shared memory.
+// States are padded to 4 L with A = B = C = 0 behind S.
 #pragma once
 
 #include "layer.h"
@@ -22,17 +18,25 @@ using namespace layer;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int LANES, int STATES, int TOKENS, int BLOCK>
-struct Tile {
-    static constexpr int L = LANES, K = STATES;
-    static constexpr int TT = TOKENS;                  // tokens per tile
-    static constexpr int THREADS = BLOCK;
-    static constexpr int CH = THREADS / L;             // channels per block
-    static constexpr int SP = K * L;                   // padded states
-    static constexpr int Q = CH / 4;                   // channel quads
-    static constexpr int IPT = (TT * Q + THREADS - 1) / THREADS;      // quads per thread
-    static constexpr int ROWS = THREADS / Q < TT ? THREADS / Q : TT;  // threads that share a quad
-    static_assert(CH % 4 == 0 && (THREADS % Q == 0) && TT % 4 == 0, "tile");
+// How a warp's lanes share the work of every pass over tokens: L lanes share
+// two channels and hold four states of each, so that what a lane reads of B and
+// C from shared memory serves eight states (a 16-byte read returns 512 bytes to
+// a warp's registers, four clocks of an SM's 128 bytes; one channel a lane would
+// spend as long on them as on the exponentials).  What depends on (token,
+// channel) alone is worked out once, by the lane that also ends up with that
+// element's sums: in a batch of TB tokens, lane l has channel l % 2 of its pair
+// and one token, and the fold over the lanes of the batch's 2 TB sums leaves
+// each lane with its own (lanes from 2 TB on have none).
+template <int LANES, int BATCH, int BLOCK>
+struct Shape {
+    static constexpr int L = LANES, THREADS = BLOCK, WARPS = BLOCK / 32;
+    static constexpr int PAIRS = 32 / L, WCH = 2 * PAIRS, CH = WCH * WARPS;  // channels of a warp, of a block
+    static constexpr int SP = 4 * L;                                        // padded states
+    static constexpr int TB = L >= 2 ? (L / 2 < BATCH ? L / 2 : BATCH) : 1;  // tokens per batch
+    static constexpr int TT = L >= 4 ? 16 : 4 * L;                          // tokens per tile
+    static constexpr int NB = TT / TB;                                      // batches per tile
+    static constexpr int OWN = L == 1 ? 2 : 1;                              // elements of a lane per batch
+    static constexpr int BITS = TB == 16 ? 4 : TB == 8 ? 3 : TB == 4 ? 2 : TB == 2 ? 1 : 0;
 };
 
 // Two fp32 values in one instruction: half the issue slots of the products and
@@ -154,11 +158,12 @@ struct Params {
     const float* init;
     T* out;
     float* fin;
-    float* ends;   // per slot [D][S]: end states, then entry states; nullptr: no unit follows another
-    float* steps;  // per slot [D]: sum of dt
+    float* ends;     // per slot [D][S]: end states, then entry states; nullptr: no unit follows another
+    float* steps;    // per slot [D]: sum of dt
+    float* entries;  // per tile [D][S]: state at the tile's entry (wanted by the backward pass)
     Units units;
     int D, S, G, Dg, cpb;  // channels, states, groups, channels and blocks per group
-    int vec_d, vec_s;      // rows of channels, of states load in fours
+    int vec_s;             // rows of states load in fours
     int softplus;
 };
 
@@ -259,27 +264,13 @@ struct StateRows {
     }
 };
 
-// Rows of one (token, channel) operand of one tile, raw.  Thread tid takes the
-// channel quad tid % Q of tokens tid / Q, tid / Q + THREADS / Q, ...: `at` is
-// its first element's offset, `left` the tokens from there to the unit's end.
-template <typename T, typename Tl>
-struct ChannelRows {
-    static constexpr int STEP = Tl::THREADS / Tl::Q;
-    Raw4<T> r[Tl::IPT];
-    __device__ __forceinline__ void load(const T* base, size_t at, int D, int left, int n, bool vec, int tid)
-    {
-#pragma unroll
-        for (int k = 0; k < Tl::IPT; ++k) {
-            r[k].zero();
-            const bool in_tile = Tl::Q * Tl::TT >= Tl::THREADS || tid / Tl::Q < Tl::TT;
-            if (in_tile && k * STEP < left && n > 0) {
-                const T* q = base + at + (size_t)(k * STEP) * D;
-                if (vec) r[k].load(q);
-                else r[k].load_some(q, n);
-            }
-        }
-    }
-};
+// Lanes that share two channels of S states.
+inline int lanes_of(int S)
+{
+    int l = 1;
+    while (4 * l < S) l <<= 1;
+    return l;
+}
 
 inline Units units_of(const int32_t* cu, int B, int T, int N, int len)
 {
@@ -352,11 +343,14 @@ Params<T> params_of(const ScanArgs& a, int len, int CH)
     p.G = a.G;
     p.Dg = a.D / a.G;
     p.cpb = (p.Dg + CH - 1) / CH;
-    p.vec_d = p.Dg % 4 == 0;
     p.vec_s = a.S % 4 == 0;
     p.softplus = a.softplus;
     return p;
 }
+
+// The forward walk with the state at every tile's entry as its only result.
+cudaError_t launch_ssm_entries(const ScanArgs& a, int len, float* ends, float* entries, kda_dtype dtype,
+                               cudaStream_t st);
 
 // Entry states of the units of every (sequence, channel, state), in place of
 // their end states.

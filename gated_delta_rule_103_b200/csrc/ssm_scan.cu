@@ -16,28 +16,17 @@ namespace {
 
 using namespace ssm;
 
-// A block is one warp and needs no barrier.  L lanes share two channels and
-// hold four states of each: what a lane reads of B and C from shared memory
-// then serves eight states (each 16-byte read returns 512 bytes to a warp's
-// registers, four clocks of an SM's 128 bytes; one channel a lane would spend as
-// long on them as on the exponentials).  What depends on (token, channel) alone
-// is worked out once, by the lane that also ends up with its output: in a batch
-// of TB = L / 2 tokens, lane l has channel l % 2 and one token, and the fold
-// over the lanes of the batch's 2 TB outputs leaves each with its own.
+// A block is one warp and needs no barrier.
 template <int LANES>
-struct Fwd {
-    static constexpr int L = LANES, THREADS = 32;
-    static constexpr int PAIRS = 32 / L, CH = 2 * PAIRS, SP = 4 * L;
-    static constexpr int TB = L >= 2 ? L / 2 : 1;          // tokens per batch
-    static constexpr int TT = L >= 4 ? 16 : 4 * L;         // tokens per tile
-    static constexpr int NB = TT / TB;                     // batches per tile
-    static constexpr int OWN = L == 1 ? 2 : 1;             // elements of a lane per batch
-    static constexpr int BITS = L == 32 ? 4 : L == 16 ? 3 : L == 8 ? 2 : L == 4 ? 1 : 0;  // log2 TB
+using Fwd = Shape<LANES, 16, 32>;
+
+enum Mode {
+    kOut,     // outputs and final states
+    kCarry,   // end state from zero and sum of dt of every unit that another one follows
+    kEntries  // the state at every tile's entry
 };
 
-// kCarry: the first pass, end state from zero and sum of dt of every unit that
-// another one follows.
-template <typename T, int LANES, bool kCarry>
+template <typename T, int LANES, Mode mode>
 __global__ void __launch_bounds__(32, 10)
 kda_ssm_scan_kernel(Params<T> p)
 {
@@ -46,7 +35,7 @@ kda_ssm_scan_kernel(Params<T> p)
     constexpr int PAIRS = Tl::PAIRS;
     __shared__ __align__(16) float2 s_dt[TT][PAIRS][2];  // dt, dt u
     __shared__ __align__(16) float s_B[TT * SP];
-    __shared__ __align__(16) float s_C[kCarry ? 4 : TT * SP];
+    __shared__ __align__(16) float s_C[mode != kOut ? 4 : TT * SP];
 
     const int lane = threadIdx.x & 31;
     const int across = p.G * p.cpb;
@@ -55,7 +44,7 @@ kda_ssm_scan_kernel(Params<T> p)
     int n, seg, t0, end;
     bool last;
     if (!p.units.locate(slot, n, seg, last, t0, end)) return;
-    if (kCarry && last) return;
+    if (mode == kCarry && last) return;
     const int cg = (gb % p.cpb) * CH;                      // first channel within the group
     const int nch = p.Dg - cg < CH ? p.Dg - cg : CH;       // channels of this block
     const int c0 = g * p.Dg + cg;
@@ -73,7 +62,7 @@ kda_ssm_scan_kernel(Params<T> p)
             const bool ok = s0 + i < p.S;
             A[r][i] = ok ? p.A[row + i] * kLog2e : 0.f;
             h[r][i] = 0.f;
-            if (ok && !kCarry) {
+            if (ok && mode != kCarry) {
                 if (p.ends) h[r][i] = p.ends[(size_t)slot * p.D * p.S + row + i];
                 else if (p.init) h[r][i] = p.init[(size_t)n * p.D * p.S + row + i];
             }
@@ -94,10 +83,10 @@ kda_ssm_scan_kernel(Params<T> p)
         skip[o] = p.skip ? p.skip[own[o]] : 0.f;
         dt_sum[o] = 0.f;
     }
-    const bool gate = !kCarry && p.z;
+    const bool gate = mode == kOut && p.z;
 
     T u[NB][OWN], d[NB][OWN], z[NB][OWN];
-    StateRows<T, Tl, !kCarry> bc;
+    StateRows<T, Tl, mode == kOut> bc;
     // the tile from token t on (tokens behind the end repeat the last)
     const size_t step = (size_t)TB * p.D;
     auto fetch = [&](int t) {
@@ -130,6 +119,15 @@ kda_ssm_scan_kernel(Params<T> p)
     if (t0 < end) fetch(t0);
     for (int t = t0; t < end; t += TT) {
         const int left = end - t < TT ? end - t : TT;
+        if constexpr (mode == kEntries) {
+            float* to = p.entries + (size_t)(t0 / TT + slot + (t - t0) / TT) * p.D * p.S;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int c = pair * 2 + r;
+                if (c < nch) store4(to + (size_t)(c0 + c) * p.S + s0, h[r], p.vec_s && s0 < p.S, p.S - s0);
+            }
+            if (t + TT >= end) break;
+        }
         float x[NB][OWN], zz[NB][OWN], dt[NB * OWN];
 #pragma unroll
         for (int e = 0; e < NB; ++e)
@@ -163,7 +161,7 @@ kda_ssm_scan_kernel(Params<T> p)
 #pragma unroll
             for (int o = 0; o < OWN; ++o) {
                 const float v = e * TB + tok < left ? dt[e * OWN + o] : 0.f;  // behind the end: a step of nothing
-                if (kCarry) dt_sum[o] += v;
+                if (mode == kCarry) dt_sum[o] += v;
                 const float w = v * x[e][o];
                 s_dt[e * TB + tok][pair][OWN == 2 ? o : lane & 1] = make_float2(v, w);
             }
@@ -177,7 +175,7 @@ kda_ssm_scan_kernel(Params<T> p)
         auto read = [&](int tt) {
             dd[tt % 3] = *reinterpret_cast<const float4*>(&s_dt[tt][pair][0]);
             B[tt % 3] = *reinterpret_cast<const float4*>(&s_B[tt * SP + s0]);
-            if constexpr (!kCarry) C[tt % 3] = *reinterpret_cast<const float4*>(&s_C[tt * SP + s0]);
+            if constexpr (mode == kOut) C[tt % 3] = *reinterpret_cast<const float4*>(&s_C[tt * SP + s0]);
         };
         auto decay = [&](int tt) {
 #pragma unroll
@@ -205,13 +203,13 @@ kda_ssm_scan_kernel(Params<T> p)
                     h[r][1] = fmaf(a[tt % 2][r][1], h[r][1], du * b.y);
                     h[r][2] = fmaf(a[tt % 2][r][2], h[r][2], du * b.z);
                     h[r][3] = fmaf(a[tt % 2][r][3], h[r][3], du * b.w);
-                    if constexpr (!kCarry) {
+                    if constexpr (mode == kOut) {
                         const float4 c = C[tt % 3];
                         y[r * TB + j] = fmaf(h[r][3], c.w, fmaf(h[r][2], c.z, fmaf(h[r][1], c.y, h[r][0] * c.x)));
                     }
                 }
             }
-            if constexpr (!kCarry) {
+            if constexpr (mode == kOut) {
                 fold<2 * TB, L, 1>(y, lane);
 #pragma unroll
                 for (int o = 0; o < OWN; ++o) {
@@ -224,8 +222,8 @@ kda_ssm_scan_kernel(Params<T> p)
         __syncwarp();
     }
 
-    if (kCarry || (last && p.fin)) {
-        float* to = kCarry ? p.ends + (size_t)slot * p.D * p.S : p.fin + (size_t)n * p.D * p.S;
+    if (mode == kCarry || (mode == kOut && last && p.fin)) {
+        float* to = mode == kCarry ? p.ends + (size_t)slot * p.D * p.S : p.fin + (size_t)n * p.D * p.S;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int c = pair * 2 + r;
@@ -234,7 +232,7 @@ kda_ssm_scan_kernel(Params<T> p)
                 if (c < nch && s0 + i < p.S) to[(size_t)(c0 + c) * p.S + s0 + i] = h[r][i];
         }
     }
-    if constexpr (kCarry) {
+    if constexpr (mode == kCarry) {
         // a channel's tokens lie with the lanes of its parity
 #pragma unroll
         for (int o = 0; o < OWN; ++o) {
@@ -380,16 +378,9 @@ kda_ssm_step_kernel(const T* __restrict__ u, const T* __restrict__ delta, const 
 // A unit's tokens are passed over twice where sequences are cut.
 constexpr int kFewWarps = 6, kWantWarps = 12, kShortest = 64;
 
-// Lanes that share two channels, and warps of one sequence's channels.
-int fwd_lanes(int S)
-{
-    int l = 1;
-    while (4 * l < S) l <<= 1;
-    return l;
-}
 Cut fwd_cut(int B, int T, int D, int S, int N, int packed)
 {
-    return cut_of(B, T, N, packed, (double)D * fwd_lanes(S) / 64.0, kFewWarps, kWantWarps, kShortest);
+    return cut_of(B, T, N, packed, (double)D * lanes_of(S) / 64.0, kFewWarps, kWantWarps, kShortest);
 }
 
 template <typename T, int L>
@@ -404,11 +395,11 @@ cudaError_t fwd(const ScanArgs& a, cudaStream_t st)
     if (c.cut) {
         p.ends = (float*)a.workspace;
         p.steps = (float*)((char*)a.workspace + round256((size_t)slots * a.D * a.S * 4));
-        kda_ssm_scan_kernel<T, L, true><<<(unsigned)blocks, 32, 0, st>>>(p);
+        kda_ssm_scan_kernel<T, L, kCarry><<<(unsigned)blocks, 32, 0, st>>>(p);
         if (cudaError_t e = cudaGetLastError()) return e;
         if (cudaError_t e = launch_ssm_chain(a.A, a.initial_state, p.ends, p.steps, p.units, a.D, a.S, st)) return e;
     }
-    kda_ssm_scan_kernel<T, L, false><<<(unsigned)blocks, 32, 0, st>>>(p);
+    kda_ssm_scan_kernel<T, L, kOut><<<(unsigned)blocks, 32, 0, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -430,10 +421,36 @@ cudaError_t step(const ScanArgs& a, cudaStream_t st)
     return cudaGetLastError();
 }
 
+template <typename T, int L>
+cudaError_t entries(const ScanArgs& a, int len, float* ends, float* to, cudaStream_t st)
+{
+    Params<T> p = params_of<T>(a, len, Fwd<L>::CH);
+    p.ends = ends;
+    p.entries = to;
+    const long long blocks = (long long)p.units.slots() * p.G * p.cpb;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    if (blocks > 0) kda_ssm_scan_kernel<T, L, kEntries><<<(unsigned)blocks, 32, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t entries_by_states(const ScanArgs& a, int len, float* ends, float* to, cudaStream_t st)
+{
+    switch (lanes_of(a.S)) {
+        case 1: return entries<T, 1>(a, len, ends, to, st);
+        case 2: return entries<T, 2>(a, len, ends, to, st);
+        case 4: return entries<T, 4>(a, len, ends, to, st);
+        case 8: return entries<T, 8>(a, len, ends, to, st);
+        case 16: return entries<T, 16>(a, len, ends, to, st);
+        case 32: return entries<T, 32>(a, len, ends, to, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
 template <typename T>
 cudaError_t fwd_by_states(const ScanArgs& a, cudaStream_t st)
 {
-    switch (fwd_lanes(a.S)) {
+    switch (lanes_of(a.S)) {
         case 1: return fwd<T, 1>(a, st);
         case 2: return fwd<T, 2>(a, st);
         case 4: return fwd<T, 4>(a, st);
@@ -458,6 +475,12 @@ cudaError_t step_by_states(const ScanArgs& a, cudaStream_t st)
 }  // namespace
 
 namespace ssm {
+cudaError_t launch_ssm_entries(const ScanArgs& a, int len, float* ends, float* to, kda_dtype dtype, cudaStream_t st)
+{
+    return dtype == KDA_DTYPE_BF16 ? entries_by_states<__nv_bfloat16>(a, len, ends, to, st)
+                                   : entries_by_states<float>(a, len, ends, to, st);
+}
+
 cudaError_t launch_ssm_chain(const float* A, const float* init, float* ends, const float* steps, const Units& units,
                              int D, int S, cudaStream_t st)
 {
