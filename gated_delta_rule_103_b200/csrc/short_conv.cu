@@ -283,15 +283,26 @@ kda_short_conv_bwd_kernel(const T* __restrict__ x, const float* __restrict__ wei
 #pragma unroll
                 for (int i = 0; i < V; ++i) part_dx[j][i] = 0.f;
             }
-            constexpr int U = 4;  // rows of x and of dy in flight per thread
+            constexpr int U = 2;  // rows of x and of dy per batch; the next batch is in flight meanwhile
+            const int last = stop + W - 1 < b ? stop + W - 1 : b;
+            Raw<T, V> nx[U], nd[U];
+            auto fetch = [&](int t) {
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    const size_t at = (size_t)(t + k < last ? t + k : last - 1) * C + c0;
+                    nx[k].load(x + at);
+                    nd[k].load(d_out + at);
+                }
+            };
+            fetch(t0);
             for (int t = t0; t < stop + W - 1; t += U) {
                 Raw<T, V> rx[U], rd[U];
 #pragma unroll
-                for (int k = 0; k < U; ++k)
-                    if (t + k < b && t + k < stop + W - 1) {
-                        rx[k].load(x + (size_t)(t + k) * C + c0);
-                        rd[k].load(d_out + (size_t)(t + k) * C + c0);
-                    }
+                for (int k = 0; k < U; ++k) {
+                    rx[k] = nx[k];
+                    rd[k] = nd[k];
+                }
+                if (t + U < last) fetch(t + U);
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
                     if (t + k >= stop + W - 1) break;

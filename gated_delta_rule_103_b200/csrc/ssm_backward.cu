@@ -343,14 +343,18 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
                 const int tt = e * TB + tok, ch = OWN == 2 ? o : lane & 1;
                 const bool in = t + tt < at.end && ch0 + ch < at.nch;  // others have no step and no adjoint
                 const float x = one(el.u[e][o]), raw = one(el.d[e][o]) + bias[o], dout = one(el.o[e][o]);
-                const float zz = p.f.z ? one(el.z[e][o]) : 0.f;
-                float dt = p.f.softplus ? softplus(raw) : raw;
+                float slope = 1.f, dt = raw, dy = dout, dz = 0.f;
+                if (p.f.softplus) dt = softplus(raw, slope);
+                if (p.f.z) {
+                    const float zz = one(el.z[e][o]), sg = sigmoid(zz);
+                    dz = dout * (sg * fmaf(zz, 1.f - sg, 1.f));
+                    dy = dout * (zz * sg);
+                }
                 if (!in) dt = 0.f;
-                const float dy = p.f.z ? dout * silu(zz) : dout;
                 if (owner) {
                     reinterpret_cast<float2*>(s_dt)[(tt * PAIRS + pair) * 2 + ch] = make_float2(dt, dt * x);
                     reinterpret_cast<float*>(s_dy)[(tt * PAIRS + pair) * 2 + ch] = in ? dy : 0.f;
-                    s_el[(e * OWN + o) * THREADS] = make_float4(x, dout, zz, raw);
+                    s_el[(e * OWN + o) * THREADS] = make_float4(x, dy, dz, slope);
                 }
             }
         bc.put(s_B, s_C, tid);
@@ -442,19 +446,13 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
 #pragma unroll
                 for (int i = 0; i < OWN; ++i) {
                     if (!mine[i] || t + tt >= at.end) continue;
-                    const float4 v = s_el[(e * OWN + i) * THREADS];  // u, d_out, z, delta + bias
+                    const float4 v = s_el[(e * OWN + i) * THREADS];  // u, dy, d_out silu'(z), softplus'
                     const float dt = reinterpret_cast<float2*>(s_dt)[(tt * PAIRS + pair) * 2 + (OWN == 2 ? i : lane & 1)].x;
                     const size_t to = (size_t)(t + tt) * D + own[i];
-                    float dy = v.y;
-                    if (p.f.z) {
-                        const float sg = sigmoid(v.z);
-                        p.gz[to] = v.y * fmaf(skip[i], v.x, o[2][i]) * (sg * fmaf(v.z, 1.f - sg, 1.f));
-                        dy = v.y * v.z * sg;
-                    }
-                    p.gu[to] = fmaf(dt, o[0][i], skip[i] * dy);
-                    sum_skip[i] = fmaf(dy, v.x, sum_skip[i]);
-                    float gd = fmaf(v.x, o[0][i], o[1][i] * kLn2);
-                    if (p.f.softplus) gd *= sigmoid(v.w);
+                    if (p.f.z) p.gz[to] = v.z * fmaf(skip[i], v.x, o[2][i]);
+                    p.gu[to] = fmaf(dt, o[0][i], skip[i] * v.y);
+                    sum_skip[i] = fmaf(v.y, v.x, sum_skip[i]);
+                    const float gd = fmaf(v.x, o[0][i], o[1][i] * kLn2) * v.w;
                     sum_bias[i] += gd;
                     p.gdelta[to] = gd;
                 }

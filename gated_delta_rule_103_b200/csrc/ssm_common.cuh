@@ -82,6 +82,14 @@ __device__ __forceinline__ float softplus(float x)
     return fmaf(2.f * r, p, fmaxf(x, 0.f));
 }
 
+// ... and its slope 1 / (1 + e^-x), which shares the exponential.
+__device__ __forceinline__ float softplus(float x, float& slope)
+{
+    const float w = fast_exp(-fabsf(x)), r1 = fast_rcp(1.f + w);
+    slope = x >= 0.f ? r1 : w * r1;
+    return softplus(x);
+}
+
 // ... of two values, the series in packed arithmetic.
 __device__ __forceinline__ float2 softplus2(float2 x)
 {
