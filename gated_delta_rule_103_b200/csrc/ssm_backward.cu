@@ -163,7 +163,7 @@ kda_ssm_bwd_carry_kernel(BwdParams<T> p)
             for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float a = ex2((r ? dd.z : dd.x) * A[r][i]);
+                    const float a = decay(r ? dd.z : dd.x, A[r][i]);
                     h[r][i] = fmaf(a, h[r][i], (r ? dd.w : dd.y) * B[i]);
                     P[r][i] *= a;
                     R[r][i] = fmaf(P[r][i], (r ? dy.y : dy.x) * C[i], R[r][i]);
@@ -329,7 +329,7 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
         for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                h[r][i] = fmaf(ex2((r ? dd.z : dd.x) * A[r][i]), h[r][i], (r ? dd.w : dd.y) * B[i]);
+                h[r][i] = fmaf(decay(r ? dd.z : dd.x, A[r][i]), h[r][i], (r ? dd.w : dd.y) * B[i]);
     };
 
     if (tiles > 0) fetch(tiles - 1);
@@ -389,7 +389,7 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
                 for (int r = 0; r < 2; ++r)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        as[j][r][i] = ex2((r ? dd.z : dd.x) * A[r][i]);
+                        as[j][r][i] = decay(r ? dd.z : dd.x, A[r][i]);
                         hs[j][r][i] = fmaf(as[j][r][i], j ? hs[j > 0 ? j - 1 : 0][r][i] : b[r][i], (r ? dd.w : dd.y) * B[i]);
                     }
             }

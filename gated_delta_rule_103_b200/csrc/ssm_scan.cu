@@ -177,15 +177,15 @@ kda_ssm_scan_kernel(Params<T> p)
             B[tt % 3] = *reinterpret_cast<const float4*>(&s_B[tt * SP + s0]);
             if constexpr (mode == kOut) C[tt % 3] = *reinterpret_cast<const float4*>(&s_C[tt * SP + s0]);
         };
-        auto decay = [&](int tt) {
+        auto decays = [&](int tt) {
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a[tt % 2][r][i] = ex2((r ? dd[tt % 3].z : dd[tt % 3].x) * A[r][i]);
+                for (int i = 0; i < 4; ++i) a[tt % 2][r][i] = decay(r ? dd[tt % 3].z : dd[tt % 3].x, A[r][i]);
         };
         read(0);
         read(1);
-        decay(0);
+        decays(0);
         size_t at = (size_t)(t + tok) * p.D;
 #pragma unroll
         for (int e = 0; e < NB; ++e, at += step) {
@@ -194,7 +194,7 @@ kda_ssm_scan_kernel(Params<T> p)
             for (int j = 0; j < TB; ++j) {
                 const int tt = e * TB + j;
                 if (tt + 2 < TT) read(tt + 2);
-                if (tt + 1 < TT) decay(tt + 1);
+                if (tt + 1 < TT) decays(tt + 1);
                 const float4 b = B[tt % 3];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
@@ -352,7 +352,7 @@ kda_ssm_step_kernel(const T* __restrict__ u, const T* __restrict__ delta, const 
         float hh[4] = {h[r].x, h[r].y, h[r].z, h[r].w}, y = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            hh[i] = fmaf(ex2(dt * a[i]), hh[i], du * B[i]);
+            hh[i] = fmaf(decay(dt, a[i]), hh[i], du * B[i]);
             y = fmaf(hh[i], C[i], y);
         }
         const bool here = live && n < N;
