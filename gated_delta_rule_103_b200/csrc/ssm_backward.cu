@@ -142,7 +142,7 @@ kda_ssm_bwd_carry_kernel(BwdParams<T> p)
                 if (p.f.z) dy *= silu(one(el.z[e][o]));
                 if (owner) {
                     dt_sum[o] += dt;
-                    s_dt[tt][pair][c] = make_float2(dt, dt * one(el.u[e][o]));
+                    s_dt[tt][pair][c] = make_float2(dt, t + tt < at.end ? dt * one(el.u[e][o]) : 0.f);
                     s_dy[tt][pair][c] = t + tt < at.end ? dy : 0.f;
                 }
             }
@@ -352,7 +352,7 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
                 }
                 if (!in) dt = 0.f;
                 if (owner) {
-                    reinterpret_cast<float2*>(s_dt)[(tt * PAIRS + pair) * 2 + ch] = make_float2(dt, dt * x);
+                    reinterpret_cast<float2*>(s_dt)[(tt * PAIRS + pair) * 2 + ch] = make_float2(dt, in ? dt * x : 0.f);
                     reinterpret_cast<float*>(s_dy)[(tt * PAIRS + pair) * 2 + ch] = in ? dy : 0.f;
                     s_el[(e * OWN + o) * THREADS] = make_float4(x, dy, dz, slope);
                 }

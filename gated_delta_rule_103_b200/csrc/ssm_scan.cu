@@ -160,9 +160,9 @@ kda_ssm_scan_kernel(Params<T> p)
         for (int e = 0; e < NB; ++e)
 #pragma unroll
             for (int o = 0; o < OWN; ++o) {
-                const float v = e * TB + tok < left ? dt[e * OWN + o] : 0.f;  // behind the end: a step of nothing
+                const bool in = e * TB + tok < left;  // behind the end: a step of nothing
+                const float v = in ? dt[e * OWN + o] : 0.f, w = in ? v * x[e][o] : 0.f;
                 if (mode == kCarry) dt_sum[o] += v;
-                const float w = v * x[e][o];
                 s_dt[e * TB + tok][pair][OWN == 2 ? o : lane & 1] = make_float2(v, w);
             }
         bc.put(s_B, s_C, lane);
@@ -284,7 +284,7 @@ kda_ssm_chain_kernel(const float* __restrict__ A, const float* __restrict__ init
 // states: whole rows of states go by in 16-byte accesses.  A thread takes its
 // channel of R sequences, whose states are in flight together and share A.
 template <typename T, int L, bool kVec, int R>
-__global__ void __launch_bounds__(256, 3)
+__global__ void __launch_bounds__(256, 4)
 kda_ssm_step_kernel(const T* __restrict__ u, const T* __restrict__ delta, const float* __restrict__ A,
                     const T* __restrict__ Bm, const T* __restrict__ Cm, const float* __restrict__ skip,
                     const T* __restrict__ z, const float* __restrict__ delta_bias, float* state,
@@ -407,13 +407,13 @@ template <typename T, int L>
 cudaError_t step(const ScanArgs& a, cudaStream_t st)
 {
     const int across = (int)(((long long)a.D * L + 255) / 256);
-    // eight sequences a thread once that still fills every SM three times
-    const int R = (long long)across * a.N >= 8LL * 3 * sm_count() ? 8 : 1;
+    // four sequences a thread once that still fills every SM's four blocks
+    const int R = (long long)across * a.N >= 4LL * 4 * sm_count() ? 4 : 1;
     const long long blocks = (long long)across * ((a.N + R - 1) / R);
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (blocks == 0) return cudaSuccess;
     const bool vec = a.S % 4 == 0;
-    auto* k = R == 8 ? (vec ? &kda_ssm_step_kernel<T, L, true, 8> : &kda_ssm_step_kernel<T, L, false, 8>)
+    auto* k = R == 4 ? (vec ? &kda_ssm_step_kernel<T, L, true, 4> : &kda_ssm_step_kernel<T, L, false, 4>)
                      : (vec ? &kda_ssm_step_kernel<T, L, true, 1> : &kda_ssm_step_kernel<T, L, false, 1>);
     k<<<(unsigned)blocks, 256, 0, st>>>((const T*)a.u, (const T*)a.delta, a.A, (const T*)a.Bm, (const T*)a.Cm, a.skip,
                                         (const T*)a.z, a.delta_bias, a.final_state, (T*)a.out, a.N, a.D, a.S,

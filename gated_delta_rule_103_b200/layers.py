@@ -100,6 +100,17 @@ def _check(status: int, where: str):
         raise KDAError(status, where)
 
 
+def _like(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """fp32 memory of an input's shape (the quickest way to allocate it)."""
+    return None if t is None else torch.empty_like(t, dtype=_F32)
+
+
+def _state(given: Optional[torch.Tensor], shape, dtype, x: torch.Tensor) -> torch.Tensor:
+    if given is not None:
+        return torch.empty_like(given, dtype=dtype)
+    return torch.empty(shape, dtype=dtype, device=x.device)
+
+
 def _space(need: int, workspace: Optional[torch.Tensor], device):
     if need == 0:
         return None, 0, None
@@ -142,7 +153,7 @@ def short_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
         if out is None:
             out = torch.empty_like(x)
         if final_state is None and output_final_state:
-            final_state = torch.empty(state, dtype=dtype, device=x.device)
+            final_state = _state(initial_state, state, dtype, x)
         _check(lib.kda_short_conv_fwd(px, pw, pb, ps, cu, _take(out, "out", x.shape, dtype),
                                       _take(final_state, "final_state", state, dtype),
                                       B, T, C, W, N, dt, flags, _raw(stream, x)), "kda_short_conv_fwd")
@@ -208,9 +219,8 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, d_out: torch.Tensor,
     shapes = ((B, T, C), (C, W), (C,), state)
     with _On(stream):
         if grads is None:
-            wanted = (True, True, bias is not None, need_initial_state_grad)
-            grads = [torch.empty(s, dtype=_F32, device=x.device) if w else None
-                     for s, w in zip(shapes, wanted)]
+            grads = (_like(x), _like(weight), _like(bias),
+                     _state(initial_state, state, _F32, x) if need_initial_state_grad else None)
         dx, dw, db, ds = grads
         if dx is None or dw is None:
             raise ValueError("grads must hold dx and dweight")
@@ -285,7 +295,7 @@ def ssm_scan_fwd(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch
         if out is None:
             out = torch.empty_like(u)
         if final_state is None and output_final_state:
-            final_state = torch.empty(state, dtype=_F32, device=u.device)
+            final_state = _state(initial_state, state, _F32, u)
         ws, size, _keep = _space(
             int(lib.kda_ssm_scan_fwd_workspace_bytes(b, T, ch, S, G, N, cu is not None, dt)), workspace,
             u.device)
@@ -344,10 +354,9 @@ def ssm_scan_bwd(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch
     shapes = (u.shape, u.shape, A.shape, B.shape, B.shape, (ch,), u.shape, (ch,), state)
     with _On(stream):
         if grads is None:
-            wanted = (True, True, True, True, True, D is not None, z is not None, delta_bias is not None,
-                      need_initial_state_grad)
-            grads = [torch.empty(s, dtype=_F32, device=u.device) if w else None
-                     for s, w in zip(shapes, wanted)]
+            grads = (_like(u), _like(u), _like(A), _like(B), _like(B), _like(D), _like(z),
+                     _like(delta_bias),
+                     _state(initial_state, state, _F32, u) if need_initial_state_grad else None)
         du, dd, dA, dB, dC, dD, dz, dbias, ds = grads
         if any(t is None for t in (du, dd, dA, dB, dC)) or (z is not None and dz is None):
             raise ValueError("grads must hold du, ddelta, dA, dB, dC and, with z, dz")
@@ -406,7 +415,7 @@ def group_norm_fwd(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] 
         if mean is None:
             mean = torch.empty(stat, dtype=_F32, device=x.device)
         if rstd is None:
-            rstd = torch.empty(stat, dtype=_F32, device=x.device)
+            rstd = torch.empty_like(mean)
         need = 0 if per_token else int(lib.kda_group_norm_fwd_workspace_bytes(
             B, T, C, groups, N, cu_seqlens is not None, dt, flags))
         ws, size, _keep = _space(need, workspace, x.device)
@@ -436,8 +445,7 @@ def group_norm_bwd(x: torch.Tensor, groups: int, d_out: torch.Tensor, mean: torc
     shapes = (x.shape, (C,), (C,))
     with _On(stream):
         if grads is None:
-            grads = [torch.empty(s, dtype=_F32, device=x.device) if w else None
-                     for s, w in zip(shapes, (True, weight is not None, bias is not None))]
+            grads = (_like(x), _like(weight), _like(bias))
         dx, dw, db = grads
         if dx is None:
             raise ValueError("grads must hold dx")
