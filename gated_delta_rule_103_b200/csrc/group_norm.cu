@@ -418,40 +418,54 @@ kda_norm_stats_kernel(const T* __restrict__ x, float* __restrict__ part, Units u
     }
 }
 
-// mean and rstd of every (sequence, group): a warp merges its units.
-__global__ void __launch_bounds__(256)
-kda_norm_merge_kernel(const float* __restrict__ part, float* __restrict__ mean, float* __restrict__ rstd,
-                      Units units, int G, int Cg, float eps)
+// Sum over a block's rows of 32 lanes, for every lane; red is [32][33].
+__device__ __forceinline__ float rows_sum(float v, float (*red)[33])
 {
-    const long long id = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (id >= (long long)units.s.N * G) return;
-    const int n = (int)(id / G), g = (int)(id % G);
+    const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
+    __syncthreads();
+    red[y][lane] = v;
+    __syncthreads();
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s += red[i][lane];
+    return s;
+}
+
+// mean and rstd of every (sequence, group): a block takes 32 groups of a
+// sequence, its 32 warps the sequence's units in turn.
+__global__ void __launch_bounds__(1024)
+kda_norm_merge_kernel(const float* __restrict__ part, float* __restrict__ mean, float* __restrict__ rstd,
+                      Units units, int G, int Cg, int across, float eps)
+{
+    __shared__ float red[32][33];
+    const int n = blockIdx.x / across, lane = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int g = (int)(blockIdx.x % across) * 32 + lane, gg = g < G ? g : G - 1;
     int a, b;
     units.s.bounds(n, a, b);
-    const int cnt = units.count_of(a, b);
-    const float* p = part + ((size_t)units.first(n) * G + g) * 2;
+    const int cnt = b > a ? units.count_of(a, b) : 0;
+    const float2* p = reinterpret_cast<const float2*>(part) + (size_t)units.first(n) * G + gg;
     const float inv = b > a ? 1.f / ((float)(b - a) * (float)Cg) : 0.f;
-    const float k = b > a ? p[0] : 0.f;
-    float s1 = 0.f, s2 = 0.f, rest = 0.f;
+    const float k = cnt ? p[0].x : 0.f;
     auto weight = [&](int i) {  // values of unit i
         const int left = b - a - i * units.len;
         return (float)(left < units.len ? left : units.len) * (float)Cg;
     };
-    if (b > a)
-        for (int i = lane; i < cnt; i += 32) s1 = fmaf(weight(i), p[(size_t)i * G * 2] - k, s1);
-    float m = fmaf(lane_sum<32>(s1), inv, k);
-    if (b > a)
-        for (int i = lane; i < cnt; i += 32) {
-            const float e = p[(size_t)i * G * 2] - m;
-            rest = fmaf(weight(i), e, rest);  // what k's rounding left of the mean
-            s2 += fmaf(weight(i) * e, e, p[(size_t)i * G * 2 + 1]);
-        }
-    s2 = lane_sum<32>(s2);
-    m = fmaf(lane_sum<32>(rest), inv, m);
-    if (lane == 0) {
-        mean[id] = m;  // 0 of an empty sequence
-        rstd[id] = 1.f / sqrtf(fmaf(s2, inv, eps));
+    float s1 = 0.f, s2 = 0.f, rest = 0.f;
+#pragma unroll 4
+    for (int i = y; i < cnt; i += 32) s1 = fmaf(weight(i), p[(size_t)i * G].x - k, s1);
+    float m = fmaf(rows_sum(s1, red), inv, k);
+#pragma unroll 4
+    for (int i = y; i < cnt; i += 32) {
+        const float2 v = p[(size_t)i * G];
+        const float e = v.x - m;
+        rest = fmaf(weight(i), e, rest);  // what k's rounding left of the mean
+        s2 += fmaf(weight(i) * e, e, v.y);
+    }
+    s2 = rows_sum(s2, red);
+    m = fmaf(rows_sum(rest, red), inv, m);
+    if (y == 0 && g < G) {
+        mean[(size_t)n * G + g] = m;  // 0 of an empty sequence
+        rstd[(size_t)n * G + g] = 1.f / sqrtf(fmaf(s2, inv, eps));
     }
 }
 
@@ -615,12 +629,12 @@ kda_norm_bwd_sums_kernel(const T* __restrict__ x, const float* __restrict__ weig
 }
 
 // From the parts: the parameters' gradients (the first blocks; 32 channels
-// each, 32 lanes over the parts), and of every (sequence, group) the means of
-// k and k xhat (the others; a warp each).
+// each, 32 warps over the parts), and of every (sequence, group) the means of
+// k and k xhat (the others; 32 groups of a sequence each).
 __global__ void __launch_bounds__(1024)
 kda_norm_bwd_merge_kernel(const float* __restrict__ part, float* __restrict__ grad_weight,
                           float* __restrict__ grad_bias, long long parts, const float* __restrict__ gsum,
-                          float* __restrict__ sums, Units units, int C, int G, int param_blocks)
+                          float* __restrict__ sums, Units units, int C, int G, int param_blocks, int across)
 {
     __shared__ float red[2][32][33];
     const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
@@ -645,24 +659,25 @@ kda_norm_bwd_merge_kernel(const float* __restrict__ part, float* __restrict__ gr
         }
         return;
     }
-    const long long id = (long long)(blockIdx.x - param_blocks) * 32 + y;
-    if (id >= (long long)units.s.N * G) return;
-    const int n = (int)(id / G), g = (int)(id % G);
+    const int at = blockIdx.x - param_blocks, n = at / across;
+    const int g = at % across * 32 + lane, gg = g < G ? g : G - 1;
     int a, b;
     units.s.bounds(n, a, b);
-    const int first = units.first(n), cnt = units.count_of(a, b);
+    const int cnt = b > a ? units.count_of(a, b) : 0;
+    const float2* p = reinterpret_cast<const float2*>(gsum) + (size_t)units.first(n) * G + gg;
     float s1 = 0.f, s2 = 0.f;
-    for (int i = lane; i < cnt; i += 32) {
-        const float2 p = *reinterpret_cast<const float2*>(gsum + ((size_t)(first + i) * G + g) * 2);
-        s1 += p.x;
-        s2 += p.y;
+#pragma unroll 4
+    for (int i = y; i < cnt; i += 32) {
+        const float2 v = p[(size_t)i * G];
+        s1 += v.x;
+        s2 += v.y;
     }
-    s1 = lane_sum<32>(s1);
-    s2 = lane_sum<32>(s2);
-    if (lane == 0) {
-        const float inv = b > a ? 1.f / ((float)(b - a) * (float)(C / G)) : 0.f;
-        sums[id * 2] = s1 * inv;
-        sums[id * 2 + 1] = s2 * inv;
+    s1 = rows_sum(s1, red[0]);
+    s2 = rows_sum(s2, red[0]);
+    if (y == 0 && g < G) {
+        const float inv = cnt ? 1.f / ((float)(b - a) * (float)(C / G)) : 0.f;
+        sums[((size_t)n * G + g) * 2] = s1 * inv;
+        sums[((size_t)n * G + g) * 2 + 1] = s2 * inv;
     }
 }
 
@@ -676,7 +691,7 @@ int width_of(int Cg, kda_dtype dtype)
 }
 
 // Blocks of up to 256 threads; units of 8 to 64 tokens per thread, the longest
-// that still give every SM eight blocks.
+// that still give every SM four blocks.
 Layout layout_of(int C, int G, int V, long long tokens)
 {
     Layout l;
@@ -694,7 +709,7 @@ Layout layout_of(int C, int G, int V, long long tokens)
     }
     l.ngb = (G + l.gb - 1) / l.gb;
     l.len = 64 * l.ty;
-    while (l.len > 8 * l.ty && tokens / l.len * l.ngb < 8LL * sm_count()) l.len >>= 1;
+    while (l.len > 8 * l.ty && tokens / l.len * l.ngb < 4LL * sm_count()) l.len >>= 1;
     return l;
 }
 
@@ -794,14 +809,15 @@ cudaError_t forward(const NormArgs& a, kda_dtype dtype, cudaStream_t st)
     }
     const Layout l = layout_of(a.C, a.G, V, (long long)a.B * a.T);
     const Units u = units_of(a.cu_seqlens, a.B, a.T, a.N, l.len);
-    const long long blocks = (long long)u.slots() * l.ngb, ng = (long long)a.N * a.G;
-    if (blocks > INT32_MAX || (ng + 7) / 8 > INT32_MAX) return cudaErrorInvalidConfiguration;
+    const int across = (a.G + 31) / 32;
+    const long long blocks = (long long)u.slots() * l.ngb, merge = (long long)a.N * across;
+    if (blocks > INT32_MAX || merge > INT32_MAX) return cudaErrorInvalidConfiguration;
     float* part = (float*)a.workspace;
     if (blocks > 0) {
         kda_norm_stats_kernel<T, V><<<(unsigned)blocks, l.threads, 0, st>>>((const T*)a.x, part, u, l, a.C, a.G);
         if (cudaError_t e = cudaGetLastError()) return e;
     }
-    kda_norm_merge_kernel<<<(unsigned)((ng + 7) / 8), 256, 0, st>>>(part, a.mean, a.rstd, u, a.G, a.C / a.G, a.eps);
+    kda_norm_merge_kernel<<<(unsigned)merge, 1024, 0, st>>>(part, a.mean, a.rstd, u, a.G, a.C / a.G, across, a.eps);
     if (cudaError_t e = cudaGetLastError()) return e;
     if (blocks > 0)
         kda_norm_apply_kernel<T, V, false><<<(unsigned)blocks, l.threads, 0, st>>>(
@@ -828,8 +844,8 @@ SumSpace sum_space(size_t slots, int C, int G, int N)
 template <typename T, int V>
 cudaError_t backward(const NormArgs& a, kda_dtype dtype, cudaStream_t st)
 {
-    const long long tokens = (long long)a.B * a.T, ng = (long long)a.N * a.G;
-    const int pblocks = (a.C + 31) / 32;
+    const long long tokens = (long long)a.B * a.T;
+    const int pblocks = (a.C + 31) / 32, across = (a.G + 31) / 32;
     float* part = (float*)a.workspace;
     if (a.per_token) {
         const RowShape r = row_shape(tokens, a.C, a.G, dtype, true);
@@ -837,12 +853,12 @@ cudaError_t backward(const NormArgs& a, kda_dtype dtype, cudaStream_t st)
             if (cudaError_t e = rows<T, V, true>(a, r, st)) return e;
         kda_norm_bwd_merge_kernel<<<(unsigned)pblocks, 1024, 0, st>>>(part, a.grad_weight, a.grad_bias,
                                                                       tokens > 0 ? r.walkers : 0, nullptr, nullptr,
-                                                                      Units{}, a.C, a.G, pblocks);
+                                                                      Units{}, a.C, a.G, pblocks, across);
         return cudaGetLastError();
     }
     const Layout l = layout_of(a.C, a.G, V, tokens);
     const Units u = units_of(a.cu_seqlens, a.B, a.T, a.N, l.len);
-    const long long slots = u.slots(), blocks = slots * l.ngb, mblocks = pblocks + (ng + 31) / 32;
+    const long long slots = u.slots(), blocks = slots * l.ngb, mblocks = pblocks + (long long)a.N * across;
     if (blocks > INT32_MAX || mblocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     const SumSpace s = sum_space((size_t)slots, a.C, a.G, a.N);
     if (blocks > 0) {
@@ -852,7 +868,8 @@ cudaError_t backward(const NormArgs& a, kda_dtype dtype, cudaStream_t st)
         if (cudaError_t e = cudaGetLastError()) return e;
     }
     kda_norm_bwd_merge_kernel<<<(unsigned)mblocks, 1024, 0, st>>>(part, a.grad_weight, a.grad_bias, slots,
-                                                                  part + s.gsum, part + s.sums, u, a.C, a.G, pblocks);
+                                                                  part + s.gsum, part + s.sums, u, a.C, a.G, pblocks,
+                                                                  across);
     if (cudaError_t e = cudaGetLastError()) return e;
     if (blocks > 0)
         kda_norm_apply_kernel<T, V, true><<<(unsigned)blocks, l.threads, 0, st>>>(
