@@ -189,24 +189,29 @@ kda_ssm_bwd_carry_kernel(BwdParams<T> p)
     }
 }
 
-// The adjoint that enters every unit from behind, in place of the one it hands
-// on: c <- exp(A sum dt) c + R, from a sequence's last unit to its first.
+// The entry states (the first half of the blocks), and the adjoint that enters
+// every unit from behind, in place of the one it hands on: c <- exp(A sum dt) c
+// + R, from a sequence's last unit to its first.
 __global__ void __launch_bounds__(256)
-kda_ssm_bwd_chain_kernel(const float* __restrict__ A, const float* __restrict__ d_fin, float* exits,
-                         const float* __restrict__ steps, Units units, int D, int S)
+kda_ssm_bwd_chain_kernel(const float* __restrict__ A, const float* __restrict__ init, float* ends,
+                         const float* __restrict__ d_fin, float* exits, const float* __restrict__ steps,
+                         Units units, int D, int S)
 {
+    const int half = gridDim.x / 2;
+    if ((int)blockIdx.x < half) {
+        chain_states(blockIdx.x, A, init, ends, steps, units, D, S);
+        return;
+    }
     const size_t DS = (size_t)D * S;
-    const int per = (int)((DS + 255) / 256);
-    const int n = (int)(blockIdx.x / per);
-    const size_t i = (size_t)(blockIdx.x % per) * 256 + threadIdx.x;
+    const int per = (int)((DS + 255) / 256), n = (blockIdx.x - half) / per;
+    const size_t i = (size_t)((blockIdx.x - half) % per) * 256 + threadIdx.x;
     if (i >= DS) return;
     const float a = A[i] * kLog2e;
-    const int first = units.first(n);
-    const int cnt = units.count(n);
+    const int first = units.first(n), cnt = units.count(n);
     float c = d_fin ? d_fin[(size_t)n * DS + i] : 0.f;
     float* e = exits + (size_t)first * DS + i;
     const float* st = steps + (size_t)first * D + i / S;
-    constexpr int U = 4;
+    constexpr int U = 8;
     for (int k = cnt - 1; k >= 0; k -= U) {
         float r[U], dt[U];
 #pragma unroll
@@ -219,7 +224,7 @@ kda_ssm_bwd_chain_kernel(const float* __restrict__ A, const float* __restrict__ 
         for (int j = 0; j < U; ++j)
             if (k - j >= 0) {
                 e[(size_t)(k - j) * DS] = c;
-                c = fmaf(ex2(a * dt[j]), c, r[j]);
+                c = fmaf(layer::ex2(a * dt[j]), c, r[j]);
             }
     }
 }
@@ -496,42 +501,41 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
     }
 }
 
-// grad_B and grad_C [tokens][G][S] from the channel blocks' sums
-// [cpb][tokens][G][2][S].  Rows in front of the first sequence or behind the
-// last belong to none and are left alone.
-__global__ void __launch_bounds__(256)
-kda_ssm_bwd_bc_kernel(const float* __restrict__ part, float* __restrict__ grad_B, float* __restrict__ grad_C,
-                      Seqs seqs, int G, int S, int cpb)
-{
-    const long long all = (long long)seqs.total * G * 2 * S;
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= all) return;
-    const long long row = i / (2 * S), t = row / G;
-    const int ws = (int)(i - row * 2 * S);
-    if (seqs.cu && (t < seqs.start(0) || t >= seqs.start(seqs.N))) return;
-    float s = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < cpb; ++k) s += part[(size_t)k * all + i];
-    if (ws < S) grad_B[row * S + ws] = s;
-    else grad_C[row * S + ws - S] = s;
-}
-
+// The first `bc_blocks` blocks: grad_B and grad_C [tokens][G][S] from the
+// channel blocks' sums [cpb][tokens][G][2][S]; rows in front of the first
+// sequence or behind the last belong to none and are left alone.  The others:
 // grad_A [D][S] (i < DS), then grad_skip and grad_delta_bias [D], from the
-// units' sums: 32 values per block, eight lanes over the units.
+// units' sums, 32 values per block, eight lanes over the units.
 __global__ void __launch_bounds__(256)
-kda_ssm_bwd_params_kernel(const float* __restrict__ part_A, const float* __restrict__ part_d,
-                          float* __restrict__ grad_A, float* __restrict__ grad_skip,
-                          float* __restrict__ grad_bias, int D, int S, long long slots)
+kda_ssm_bwd_sums_kernel(const float* __restrict__ part_bc, float* __restrict__ grad_B, float* __restrict__ grad_C,
+                        Seqs seqs, int G, int cpb, int bc_blocks, const float* __restrict__ part_A,
+                        const float* __restrict__ part_d, float* __restrict__ grad_A,
+                        float* __restrict__ grad_skip, float* __restrict__ grad_bias, int D, int S, int slots)
 {
     __shared__ float red[8][33];
+    if ((int)blockIdx.x < bc_blocks) {
+        const long long all = (long long)seqs.total * G * 2 * S;
+        const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+        if (i >= all) return;
+        const long long row = i / (2 * S), t = row / G;
+        const int ws = (int)(i - row * 2 * S);
+        if (seqs.cu && (t < seqs.start(0) || t >= seqs.start(seqs.N))) return;
+        float s = 0.f;
+#pragma unroll 8
+        for (int k = 0; k < cpb; ++k) s += part_bc[(size_t)k * all + i];
+        if (ws < S) grad_B[row * S + ws] = s;
+        else grad_C[row * S + ws - S] = s;
+        return;
+    }
     const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const long long DS = (long long)D * S, i = (long long)blockIdx.x * 32 + lane;
+    const long long DS = (long long)D * S, i = (long long)(blockIdx.x - bc_blocks) * 32 + lane;
     const bool isA = i < DS, live = i < DS + 2 * D;
     const float* src = isA ? part_A + i : part_d + (i - DS);
     const size_t stride = isA ? (size_t)DS : (size_t)2 * D;
     float s = 0.f;
     if (live)
-        for (long long k = y; k < slots; k += 8) s += src[(size_t)k * stride];
+#pragma unroll 4
+        for (int k = y; k < slots; k += 8) s += src[(size_t)k * stride];
     red[y][lane] = s;
     __syncthreads();
     if (y == 0 && live) {
@@ -549,7 +553,7 @@ kda_ssm_bwd_params_kernel(const float* __restrict__ part_A, const float* __restr
 
 // Sequences are cut where the chains give the SMs fewer warps than this: two
 // more walks then go over most tokens, a third of the whole.
-constexpr int kBwdFewWarps = 5, kBwdWantWarps = 8, kBwdShortest = 64;
+constexpr int kBwdFewWarps = 5, kBwdWantWarps = 16, kBwdShortest = 32;
 
 struct Layout {
     Cut c;
@@ -607,7 +611,8 @@ cudaError_t bwd(const ScanArgs& a, kda_dtype dtype, cudaStream_t st)
     const long long blocks = (long long)l.slots * p.f.G * p.f.cpb;
     const long long chain = ((long long)a.D * a.S + 255) / 256 * a.N;
     const long long bc = ((long long)a.B * a.T * a.G * 2 * a.S + 255) / 256;
-    if (blocks > INT32_MAX || chain > INT32_MAX || bc > INT32_MAX) return cudaErrorInvalidConfiguration;
+    const long long params = ((long long)a.D * (a.S + 2) + 31) / 32;
+    if (blocks > INT32_MAX || 2 * chain > INT32_MAX || bc + params > INT32_MAX) return cudaErrorInvalidConfiguration;
     constexpr size_t smem = sizeof(float) * BwdSpace<Bwd<L>>::kAll;
     if (cudaError_t e = cudaFuncSetAttribute(kda_ssm_bwd_kernel<T, L>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)smem))
@@ -620,23 +625,17 @@ cudaError_t bwd(const ScanArgs& a, kda_dtype dtype, cudaStream_t st)
             if (carry > INT32_MAX) return cudaErrorInvalidConfiguration;
             kda_ssm_bwd_carry_kernel<T, L><<<(unsigned)carry, 32, 0, st>>>(q);
             if (cudaError_t e = cudaGetLastError()) return e;
-            if (cudaError_t e = launch_ssm_chain(a.A, a.initial_state, p.f.ends, p.f.steps, p.f.units, a.D, a.S, st))
-                return e;
-            kda_ssm_bwd_chain_kernel<<<(unsigned)chain, 256, 0, st>>>(a.A, a.d_final_state, p.exits, p.f.steps,
-                                                                     p.f.units, a.D, a.S);
+            kda_ssm_bwd_chain_kernel<<<(unsigned)(2 * chain), 256, 0, st>>>(
+                a.A, a.initial_state, p.f.ends, a.d_final_state, p.exits, p.f.steps, p.f.units, a.D, a.S);
             if (cudaError_t e = cudaGetLastError()) return e;
         }
         if (cudaError_t e = launch_ssm_entries(a, l.c.len, p.f.ends, p.f.entries, dtype, st)) return e;
         kda_ssm_bwd_kernel<T, L><<<(unsigned)blocks, Bwd<L>::THREADS, smem, st>>>(p);
         if (cudaError_t e = cudaGetLastError()) return e;
     }
-    if (bc > 0) {
-        kda_ssm_bwd_bc_kernel<<<(unsigned)bc, 256, 0, st>>>(p.part_bc, a.grad_B, a.grad_C, p.f.units.s, a.G, a.S,
-                                                            p.f.cpb);
-        if (cudaError_t e = cudaGetLastError()) return e;
-    }
-    kda_ssm_bwd_params_kernel<<<(unsigned)(((long long)a.D * (a.S + 2) + 31) / 32), 256, 0, st>>>(
-        p.part_A, p.part_d, a.grad_A, a.grad_skip, a.grad_delta_bias, a.D, a.S, (long long)l.slots);
+    kda_ssm_bwd_sums_kernel<<<(unsigned)(bc + params), 256, 0, st>>>(
+        p.part_bc, a.grad_B, a.grad_C, p.f.units.s, a.G, p.f.cpb, (int)bc, p.part_A, p.part_d, a.grad_A, a.grad_skip,
+        a.grad_delta_bias, a.D, a.S, (int)l.slots);
     return cudaGetLastError();
 }
 

@@ -280,6 +280,40 @@ struct StateRows {
     }
 };
 
+// Entry states of the units of every (sequence, channel, state), in place of
+// their end states: h <- exp(A sum dt) h + e, unit after unit.  256 threads,
+// ceil(D S / 256) blocks a sequence.
+__device__ __forceinline__ void chain_states(int block, const float* __restrict__ A,
+                                             const float* __restrict__ init, float* ends,
+                                             const float* __restrict__ steps, const Units& units, int D, int S)
+{
+    const size_t DS = (size_t)D * S;
+    const int per = (int)((DS + 255) / 256), n = block / per;
+    const size_t i = (size_t)(block % per) * 256 + threadIdx.x;
+    if (i >= DS) return;
+    const float a = A[i] * kLog2e;
+    const int first = units.first(n), cnt = units.count(n);
+    float h = init ? init[(size_t)n * DS + i] : 0.f;
+    float* e = ends + (size_t)first * DS + i;
+    const float* st = steps + (size_t)first * D + i / S;
+    constexpr int U = 8;
+    for (int k = 0; k < cnt; k += U) {
+        float end[U], dt[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const bool ok = k + j + 1 < cnt;  // the last unit's end is no one's entry
+            end[j] = ok ? e[(size_t)(k + j) * DS] : 0.f;
+            dt[j] = ok ? st[(size_t)(k + j) * D] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (k + j < cnt) {
+                e[(size_t)(k + j) * DS] = h;
+                h = fmaf(layer::ex2(a * dt[j]), h, end[j]);
+            }
+    }
+}
+
 // Lanes that share two channels of S states.
 inline int lanes_of(int S)
 {
@@ -367,11 +401,6 @@ Params<T> params_of(const ScanArgs& a, int len, int CH)
 // The forward walk with the state at every tile's entry as its only result.
 cudaError_t launch_ssm_entries(const ScanArgs& a, int len, float* ends, float* entries, kda_dtype dtype,
                                cudaStream_t st);
-
-// Entry states of the units of every (sequence, channel, state), in place of
-// their end states.
-cudaError_t launch_ssm_chain(const float* A, const float* init, float* ends, const float* steps, const Units& units,
-                             int D, int S, cudaStream_t st);
 
 }  // namespace ssm
 }  // namespace kda

@@ -243,40 +243,11 @@ kda_ssm_scan_kernel(Params<T> p)
     }
 }
 
-// Entry states of the units of every (sequence, channel, state), in place of
-// their end states: h <- exp(A sum dt) h + e, unit after unit.
 __global__ void __launch_bounds__(256)
 kda_ssm_chain_kernel(const float* __restrict__ A, const float* __restrict__ init, float* ends,
                      const float* __restrict__ steps, Units units, int D, int S)
 {
-    const size_t DS = (size_t)D * S;
-    const int per = (int)((DS + 255) / 256);
-    const int n = (int)(blockIdx.x / per);
-    const size_t i = (size_t)(blockIdx.x % per) * 256 + threadIdx.x;
-    if (i >= DS) return;
-    const float a = A[i] * kLog2e;
-    const size_t d = i / S;
-    const int first = units.first(n);
-    const int cnt = units.count(n);
-    float h = init ? init[(size_t)n * DS + i] : 0.f;
-    float* e = ends + (size_t)first * DS + i;
-    const float* st = steps + (size_t)first * D + d;
-    constexpr int U = 4;
-    for (int k = 0; k < cnt; k += U) {
-        float end[U], dt[U];
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const bool ok = k + j + 1 < cnt;  // the last unit's end is no one's entry
-            end[j] = ok ? e[(size_t)(k + j) * DS] : 0.f;
-            dt[j] = ok ? st[(size_t)(k + j) * D] : 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-            if (k + j < cnt) {
-                e[(size_t)(k + j) * DS] = h;
-                h = fmaf(ex2(a * dt[j]), h, end[j]);
-            }
-    }
+    chain_states(blockIdx.x, A, init, ends, steps, units, D, S);
 }
 
 // One token for each of N sequences, the state read and written once in place
@@ -390,14 +361,17 @@ cudaError_t fwd(const ScanArgs& a, cudaStream_t st)
     Params<T> p = params_of<T>(a, c.len, Fwd<L>::CH);
     const int slots = p.units.slots();
     const long long blocks = (long long)slots * p.G * p.cpb;
-    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    const long long chain = ((long long)a.D * a.S + 255) / 256 * a.N;
+    if (blocks > INT32_MAX || chain > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (blocks == 0) return cudaSuccess;
     if (c.cut) {
         p.ends = (float*)a.workspace;
         p.steps = (float*)((char*)a.workspace + round256((size_t)slots * a.D * a.S * 4));
         kda_ssm_scan_kernel<T, L, kCarry><<<(unsigned)blocks, 32, 0, st>>>(p);
         if (cudaError_t e = cudaGetLastError()) return e;
-        if (cudaError_t e = launch_ssm_chain(a.A, a.initial_state, p.ends, p.steps, p.units, a.D, a.S, st)) return e;
+        kda_ssm_chain_kernel<<<(unsigned)chain, 256, 0, st>>>(a.A, a.initial_state, p.ends, p.steps, p.units, a.D,
+                                                             a.S);
+        if (cudaError_t e = cudaGetLastError()) return e;
     }
     kda_ssm_scan_kernel<T, L, kOut><<<(unsigned)blocks, 32, 0, st>>>(p);
     return cudaGetLastError();
@@ -481,14 +455,6 @@ cudaError_t launch_ssm_entries(const ScanArgs& a, int len, float* ends, float* t
                                    : entries_by_states<float>(a, len, ends, to, st);
 }
 
-cudaError_t launch_ssm_chain(const float* A, const float* init, float* ends, const float* steps, const Units& units,
-                             int D, int S, cudaStream_t st)
-{
-    const long long blocks = ((long long)D * S + 255) / 256 * units.s.N;
-    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-    kda_ssm_chain_kernel<<<(unsigned)blocks, 256, 0, st>>>(A, init, ends, steps, units, D, S);
-    return cudaGetLastError();
-}
 }  // namespace ssm
 
 size_t scan_fwd_workspace(int B, int T, int D, int S, int, int N, int packed, kda_dtype)

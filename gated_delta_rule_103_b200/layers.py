@@ -100,6 +100,11 @@ def _check(status: int, where: str):
         raise KDAError(status, where)
 
 
+def _given(grads, shapes):
+    """Checked addresses of the caller's gradients."""
+    return [_take(t, "grads", s, _F32) for t, s in zip(grads, shapes)]
+
+
 def _like(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
     """fp32 memory of an input's shape (the quickest way to allocate it)."""
     return None if t is None else torch.empty_like(t, dtype=_F32)
@@ -218,13 +223,14 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, d_out: torch.Tensor,
            _take(d_out, "d_out", x.shape, dtype), _take(d_final_state, "d_final_state", state, _F32))
     shapes = ((B, T, C), (C, W), (C,), state)
     with _On(stream):
-        if grads is None:
+        given = grads is not None
+        if not given:
             grads = (_like(x), _like(weight), _like(bias),
                      _state(initial_state, state, _F32, x) if need_initial_state_grad else None)
         dx, dw, db, ds = grads
         if dx is None or dw is None:
             raise ValueError("grads must hold dx and dweight")
-        outs = [_take(t, "grads", s, _F32) for t, s in zip(grads, shapes)]
+        outs = _given(grads, shapes) if given else [None if t is None else t.data_ptr() for t in grads]
         ws, size, _keep = _space(
             int(lib.kda_short_conv_bwd_workspace_bytes(B, T, C, W, N, cu is not None, dt)), workspace,
             x.device)
@@ -353,14 +359,15 @@ def ssm_scan_bwd(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch
             _take(d_final_state, "d_final_state", state, _F32))
     shapes = (u.shape, u.shape, A.shape, B.shape, B.shape, (ch,), u.shape, (ch,), state)
     with _On(stream):
-        if grads is None:
+        given = grads is not None
+        if not given:
             grads = (_like(u), _like(u), _like(A), _like(B), _like(B), _like(D), _like(z),
                      _like(delta_bias),
                      _state(initial_state, state, _F32, u) if need_initial_state_grad else None)
         du, dd, dA, dB, dC, dD, dz, dbias, ds = grads
         if any(t is None for t in (du, dd, dA, dB, dC)) or (z is not None and dz is None):
             raise ValueError("grads must hold du, ddelta, dA, dB, dC and, with z, dz")
-        outs = [_take(t, "grads", s, _F32) for t, s in zip(grads, shapes)]
+        outs = _given(grads, shapes) if given else [None if t is None else t.data_ptr() for t in grads]
         ws, size, _keep = _space(
             int(lib.kda_ssm_scan_bwd_workspace_bytes(b, T, ch, S, G, N, cu is not None, dt)), workspace,
             u.device)
@@ -444,12 +451,13 @@ def group_norm_bwd(x: torch.Tensor, groups: int, d_out: torch.Tensor, mean: torc
             _take(d_out, "d_out", x.shape, x.dtype))
     shapes = (x.shape, (C,), (C,))
     with _On(stream):
-        if grads is None:
+        given = grads is not None
+        if not given:
             grads = (_like(x), _like(weight), _like(bias))
         dx, dw, db = grads
         if dx is None:
             raise ValueError("grads must hold dx")
-        outs = [_take(t, "grads", s, _F32) for t, s in zip(grads, shapes)]
+        outs = _given(grads, shapes) if given else [None if t is None else t.data_ptr() for t in grads]
         ws, size, _keep = _space(
             int(lib.kda_group_norm_bwd_workspace_bytes(B, T, C, groups, N, cu_seqlens is not None, dt, flags)),
             workspace, x.device)
