@@ -27,7 +27,7 @@ enum Mode {
 };
 
 template <typename T, int LANES, Mode mode>
-__global__ void __launch_bounds__(32, 10)
+__global__ void __launch_bounds__(32, 11)
 kda_ssm_scan_kernel(Params<T> p)
 {
     using Tl = Fwd<LANES>;
@@ -347,7 +347,7 @@ kda_ssm_step_kernel(const T* __restrict__ u, const T* __restrict__ delta, const 
 }
 
 // A unit's tokens are passed over twice where sequences are cut.
-constexpr int kFewWarps = 6, kWantWarps = 12, kShortest = 64;
+constexpr int kFewWarps = 6, kWantWarps = 16, kShortest = 32;
 
 Cut fwd_cut(int B, int T, int D, int S, int N, int packed)
 {
