@@ -195,37 +195,40 @@ kda_ssm_bwd_carry_kernel(BwdParams<T> p)
 __global__ void __launch_bounds__(256)
 kda_ssm_bwd_chain_kernel(const float* __restrict__ A, const float* __restrict__ init, float* ends,
                          const float* __restrict__ d_fin, float* exits, const float* __restrict__ steps,
-                         Units units, int D, int S)
+                         Units units, int D, int S, int span)
 {
     const int half = gridDim.x / 2;
     if ((int)blockIdx.x < half) {
-        chain_states(blockIdx.x, A, init, ends, steps, units, D, S);
+        chain_states(blockIdx.x, A, init, ends, steps, units, D, S, span);
         return;
     }
     const size_t DS = (size_t)D * S;
-    const int per = (int)((DS + 255) / 256), n = (blockIdx.x - half) / per;
-    const size_t i = (size_t)((blockIdx.x - half) % per) * 256 + threadIdx.x;
-    if (i >= DS) return;
-    const float a = A[i] * kLog2e;
-    const int first = units.first(n), cnt = units.count(n);
-    float c = d_fin ? d_fin[(size_t)n * DS + i] : 0.f;
-    float* e = exits + (size_t)first * DS + i;
-    const float* st = steps + (size_t)first * D + i / S;
-    constexpr int U = 8;
-    for (int k = cnt - 1; k >= 0; k -= U) {
-        float r[U], dt[U];
+    const int per = (int)((DS + span - 1) / span), n = (blockIdx.x - half) / per;
+    const int cnt = units.count(n);
+    if (cnt == 1) return;  // a sequence's last unit has the final state's adjoint
+    const int first = units.first(n);
+    const size_t i0 = (size_t)((blockIdx.x - half) % per) * span, i1 = i0 + span < DS ? i0 + span : DS;
+    for (size_t i = i0 + threadIdx.x; i < i1; i += 256) {
+        const float a = A[i] * kLog2e;
+        float c = d_fin ? d_fin[(size_t)n * DS + i] : 0.f;
+        float* e = exits + (size_t)first * DS + i;
+        const float* st = steps + (size_t)first * D + (unsigned)i / (unsigned)S;
+        constexpr int U = 8;
+        for (int k = cnt - 1; k >= 0; k -= U) {
+            float r[U], dt[U];
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const bool ok = k - j > 0;  // the first unit hands on to no one
-            r[j] = ok ? e[(size_t)(k - j) * DS] : 0.f;
-            dt[j] = ok ? st[(size_t)(k - j) * D] : 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-            if (k - j >= 0) {
-                e[(size_t)(k - j) * DS] = c;
-                c = fmaf(layer::ex2(a * dt[j]), c, r[j]);
+            for (int j = 0; j < U; ++j) {
+                const bool ok = k - j > 0;  // the first unit hands on to no one
+                r[j] = ok ? e[(size_t)(k - j) * DS] : 0.f;
+                dt[j] = ok ? st[(size_t)(k - j) * D] : 0.f;
             }
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (k - j >= 0) {
+                    e[(size_t)(k - j) * DS] = c;
+                    c = fmaf(layer::ex2(a * dt[j]), c, r[j]);
+                }
+        }
     }
 }
 
@@ -340,6 +343,7 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
     if (tiles > 0) fetch(tiles - 1);
     for (int k = tiles - 1; k >= 0; --k) {
         const int t = at.t0 + k * TT;
+        const int fours = at.end - t < TT ? (at.end - t + 3) / 4 : TT / 4;  // with a token in them
         // what depends on (token, channel) alone
 #pragma unroll
         for (int e = 0; e < NB; ++e)
@@ -369,9 +373,9 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
         for (int q = 0; q < TT / 4; ++q) {
             s_m[(2 * q) * THREADS] = make_float4(h[0][0], h[0][1], h[0][2], h[0][3]);
             s_m[(2 * q + 1) * THREADS] = make_float4(h[1][0], h[1][1], h[1][2], h[1][3]);
-            if (q + 1 < TT / 4)
+            if (q + 1 >= fours) break;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) advance(q * 4 + j);
+            for (int j = 0; j < 4; ++j) advance(q * 4 + j);
         }
         if (k > 0) fetch(k - 1);
         // a tile's sum of dA first: long sums of small terms keep their digits
@@ -381,7 +385,7 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
 #pragma unroll
             for (int i = 0; i < 4; ++i) dA_t[r][i] = 0.f;
 #pragma unroll 1
-        for (int q = TT / 4 - 1; q >= 0; --q) {
+        for (int q = fours - 1; q >= 0; --q) {
             const float4 m0 = s_m[(2 * q) * THREADS], m1 = s_m[(2 * q + 1) * THREADS];
             const float b[2][4] = {{m0.x, m0.y, m0.z, m0.w}, {m1.x, m1.y, m1.z, m1.w}};
             float hs[4][2][4], as[4][2][4];
@@ -609,10 +613,10 @@ cudaError_t bwd(const ScanArgs& a, kda_dtype dtype, cudaStream_t st)
     p.part_A = (float*)(ws + l.A);
     p.part_d = (float*)(ws + l.d);
     const long long blocks = (long long)l.slots * p.f.G * p.f.cpb;
-    const long long chain = ((long long)a.D * a.S + 255) / 256 * a.N;
+    const ChainGrid chain = chain_grid(a.D, a.S, a.N);
     const long long bc = ((long long)a.B * a.T * a.G * 2 * a.S + 255) / 256;
     const long long params = ((long long)a.D * (a.S + 2) + 31) / 32;
-    if (blocks > INT32_MAX || 2 * chain > INT32_MAX || bc + params > INT32_MAX) return cudaErrorInvalidConfiguration;
+    if (blocks > INT32_MAX || 2 * chain.blocks > INT32_MAX || bc + params > INT32_MAX) return cudaErrorInvalidConfiguration;
     constexpr size_t smem = sizeof(float) * BwdSpace<Bwd<L>>::kAll;
     if (cudaError_t e = cudaFuncSetAttribute(kda_ssm_bwd_kernel<T, L>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)smem))
@@ -625,8 +629,9 @@ cudaError_t bwd(const ScanArgs& a, kda_dtype dtype, cudaStream_t st)
             if (carry > INT32_MAX) return cudaErrorInvalidConfiguration;
             kda_ssm_bwd_carry_kernel<T, L><<<(unsigned)carry, 32, 0, st>>>(q);
             if (cudaError_t e = cudaGetLastError()) return e;
-            kda_ssm_bwd_chain_kernel<<<(unsigned)(2 * chain), 256, 0, st>>>(
-                a.A, a.initial_state, p.f.ends, a.d_final_state, p.exits, p.f.steps, p.f.units, a.D, a.S);
+            kda_ssm_bwd_chain_kernel<<<(unsigned)(2 * chain.blocks), 256, 0, st>>>(
+                a.A, a.initial_state, p.f.ends, a.d_final_state, p.exits, p.f.steps, p.f.units, a.D, a.S,
+                chain.span);
             if (cudaError_t e = cudaGetLastError()) return e;
         }
         if (cudaError_t e = launch_ssm_entries(a, l.c.len, p.f.ends, p.f.entries, dtype, st)) return e;

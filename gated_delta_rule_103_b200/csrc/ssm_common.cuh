@@ -282,35 +282,52 @@ struct StateRows {
 
 // Entry states of the units of every (sequence, channel, state), in place of
 // their end states: h <- exp(A sum dt) h + e, unit after unit.  256 threads,
-// ceil(D S / 256) blocks a sequence.
+// `span` values a block: one a thread, or four where there are blocks enough
+// (most blocks of many short sequences find one unit and nothing to do).
+struct ChainGrid {
+    int span;
+    long long blocks;
+};
+inline ChainGrid chain_grid(int D, int S, int N)
+{
+    const long long DS = (long long)D * S, blocks = (DS + 255) / 256 * N;
+    ChainGrid c = {blocks > 32LL * sm_count() ? 1024 : 256, 0};
+    c.blocks = (DS + c.span - 1) / c.span * N;
+    return c;
+}
+
 __device__ __forceinline__ void chain_states(int block, const float* __restrict__ A,
                                              const float* __restrict__ init, float* ends,
-                                             const float* __restrict__ steps, const Units& units, int D, int S)
+                                             const float* __restrict__ steps, const Units& units, int D, int S,
+                                             int span)
 {
     const size_t DS = (size_t)D * S;
-    const int per = (int)((DS + 255) / 256), n = block / per;
-    const size_t i = (size_t)(block % per) * 256 + threadIdx.x;
-    if (i >= DS) return;
-    const float a = A[i] * kLog2e;
-    const int first = units.first(n), cnt = units.count(n);
-    float h = init ? init[(size_t)n * DS + i] : 0.f;
-    float* e = ends + (size_t)first * DS + i;
-    const float* st = steps + (size_t)first * D + i / S;
-    constexpr int U = 8;
-    for (int k = 0; k < cnt; k += U) {
-        float end[U], dt[U];
+    const int per = (int)((DS + span - 1) / span), n = block / per;
+    const int cnt = units.count(n);
+    if (cnt == 1) return;  // a sequence's first unit begins from its initial state
+    const int first = units.first(n);
+    const size_t i0 = (size_t)(block % per) * span, i1 = i0 + span < DS ? i0 + span : DS;
+    for (size_t i = i0 + threadIdx.x; i < i1; i += 256) {
+        const float a = A[i] * kLog2e;
+        float h = init ? init[(size_t)n * DS + i] : 0.f;
+        float* e = ends + (size_t)first * DS + i;
+        const float* st = steps + (size_t)first * D + (unsigned)i / (unsigned)S;
+        constexpr int U = 8;
+        for (int k = 0; k < cnt; k += U) {
+            float end[U], dt[U];
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const bool ok = k + j + 1 < cnt;  // the last unit's end is no one's entry
-            end[j] = ok ? e[(size_t)(k + j) * DS] : 0.f;
-            dt[j] = ok ? st[(size_t)(k + j) * D] : 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-            if (k + j < cnt) {
-                e[(size_t)(k + j) * DS] = h;
-                h = fmaf(layer::ex2(a * dt[j]), h, end[j]);
+            for (int j = 0; j < U; ++j) {
+                const bool ok = k + j + 1 < cnt;  // the last unit's end is no one's entry
+                end[j] = ok ? e[(size_t)(k + j) * DS] : 0.f;
+                dt[j] = ok ? st[(size_t)(k + j) * D] : 0.f;
             }
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (k + j < cnt) {
+                    e[(size_t)(k + j) * DS] = h;
+                    h = fmaf(layer::ex2(a * dt[j]), h, end[j]);
+                }
+        }
     }
 }
 
@@ -359,9 +376,10 @@ inline Cut cut_of(int B, int T, int N, int packed, double chain_warps, int few, 
     const double units = (double)sm_count() * want / chain_warps;
     double len = (double)tokens / (units < 1.0 ? 1.0 : units);
     if (packed) {
-        // the longest sequence is not known here: no unit is longer than twice
-        // the mean, and where there are many chains none shorter
-        const double mean = 2.0 * (double)tokens / N;
+        // The longest sequence is not known here, and the whole call would wait
+        // for it: no unit is longer than the mean, and where there are many
+        // chains none shorter (sequences of one length then stay whole).
+        const double mean = (double)tokens / N;
         if (many || len > mean) len = mean;
     }
     long long l = ((long long)len + 15) / 16 * 16;

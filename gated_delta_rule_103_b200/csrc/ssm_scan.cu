@@ -63,7 +63,7 @@ kda_ssm_scan_kernel(Params<T> p)
             A[r][i] = ok ? p.A[row + i] * kLog2e : 0.f;
             h[r][i] = 0.f;
             if (ok && mode != kCarry) {
-                if (p.ends) h[r][i] = p.ends[(size_t)slot * p.D * p.S + row + i];
+                if (p.ends && seg > 0) h[r][i] = p.ends[(size_t)slot * p.D * p.S + row + i];
                 else if (p.init) h[r][i] = p.init[(size_t)n * p.D * p.S + row + i];
             }
         }
@@ -245,9 +245,9 @@ kda_ssm_scan_kernel(Params<T> p)
 
 __global__ void __launch_bounds__(256)
 kda_ssm_chain_kernel(const float* __restrict__ A, const float* __restrict__ init, float* ends,
-                     const float* __restrict__ steps, Units units, int D, int S)
+                     const float* __restrict__ steps, Units units, int D, int S, int span)
 {
-    chain_states(blockIdx.x, A, init, ends, steps, units, D, S);
+    chain_states(blockIdx.x, A, init, ends, steps, units, D, S, span);
 }
 
 // One token for each of N sequences, the state read and written once in place
@@ -361,16 +361,16 @@ cudaError_t fwd(const ScanArgs& a, cudaStream_t st)
     Params<T> p = params_of<T>(a, c.len, Fwd<L>::CH);
     const int slots = p.units.slots();
     const long long blocks = (long long)slots * p.G * p.cpb;
-    const long long chain = ((long long)a.D * a.S + 255) / 256 * a.N;
-    if (blocks > INT32_MAX || chain > INT32_MAX) return cudaErrorInvalidConfiguration;
+    const ChainGrid chain = chain_grid(a.D, a.S, a.N);
+    if (blocks > INT32_MAX || chain.blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (blocks == 0) return cudaSuccess;
     if (c.cut) {
         p.ends = (float*)a.workspace;
         p.steps = (float*)((char*)a.workspace + round256((size_t)slots * a.D * a.S * 4));
         kda_ssm_scan_kernel<T, L, kCarry><<<(unsigned)blocks, 32, 0, st>>>(p);
         if (cudaError_t e = cudaGetLastError()) return e;
-        kda_ssm_chain_kernel<<<(unsigned)chain, 256, 0, st>>>(a.A, a.initial_state, p.ends, p.steps, p.units, a.D,
-                                                             a.S);
+        kda_ssm_chain_kernel<<<(unsigned)chain.blocks, 256, 0, st>>>(a.A, a.initial_state, p.ends, p.steps, p.units,
+                                                                    a.D, a.S, chain.span);
         if (cudaError_t e = cudaGetLastError()) return e;
     }
     kda_ssm_scan_kernel<T, L, kOut><<<(unsigned)blocks, 32, 0, st>>>(p);
