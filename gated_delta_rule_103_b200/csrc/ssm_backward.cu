@@ -417,19 +417,31 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const float dt = r ? dd.z : dd.x, du = r ? dd.w : dd.y, dy = r ? dy2.y : dy2.x;
-                        float gB = 0.f, wA = 0.f, hC = 0.f;
+                        float2 sB = both(0.f), sA = sB, sC = sB;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float gg = fmaf(C[i], dy, c[r][i]);
-                            c[r][i] = as[j][r][i] * gg;
-                            const float w = c[r][i] * (j ? hs[j > 0 ? j - 1 : 0][r][i] : b[r][i]);
-                            dA_t[r][i] = fmaf(w, dt, dA_t[r][i]);
-                            gB = fmaf(gg, B[i], gB);
-                            wA = fmaf(w, A[r][i], wA);
-                            hC = fmaf(hs[j][r][i], C[i], hC);
-                            bc8[i] = r ? fmaf(gg, du, bc8[i]) : gg * du;
-                            bc8[4 + i] = r ? fmaf(hs[j][r][i], dy, bc8[4 + i]) : hs[j][r][i] * dy;
+                        for (int i = 0; i < 4; i += 2) {
+                            // the recurrence in scalars (shorter latency), the sums in pairs
+                            const float g0 = fmaf(C[i], dy, c[r][i]), g1 = fmaf(C[i + 1], dy, c[r][i + 1]);
+                            c[r][i] = as[j][r][i] * g0;
+                            c[r][i + 1] = as[j][r][i + 1] * g1;
+                            const float2 gg = make_float2(g0, g1), h2 = make_float2(hs[j][r][i], hs[j][r][i + 1]);
+                            const float2 hp = j ? make_float2(hs[j > 0 ? j - 1 : 0][r][i], hs[j > 0 ? j - 1 : 0][r][i + 1])
+                                                : make_float2(b[r][i], b[r][i + 1]);
+                            const float2 w = mul2(make_float2(c[r][i], c[r][i + 1]), hp);
+                            const float2 da = fma2(w, both(dt), make_float2(dA_t[r][i], dA_t[r][i + 1]));
+                            dA_t[r][i] = da.x;
+                            dA_t[r][i + 1] = da.y;
+                            sB = fma2(gg, make_float2(B[i], B[i + 1]), sB);
+                            sA = fma2(w, make_float2(A[r][i], A[r][i + 1]), sA);
+                            sC = fma2(h2, make_float2(C[i], C[i + 1]), sC);
+                            const float2 pb = r ? fma2(gg, both(du), make_float2(bc8[i], bc8[i + 1])) : mul2(gg, both(du));
+                            const float2 pc = r ? fma2(h2, both(dy), make_float2(bc8[4 + i], bc8[5 + i])) : mul2(h2, both(dy));
+                            bc8[i] = pb.x;
+                            bc8[i + 1] = pb.y;
+                            bc8[4 + i] = pc.x;
+                            bc8[5 + i] = pc.y;
                         }
+                        const float gB = sB.x + sB.y, wA = sA.x + sA.y, hC = sC.x + sC.y;
                         o[0][r * TB + jj] = gB;
                         o[1][r * TB + jj] = wA;
                         o[2][r * TB + jj] = hC;

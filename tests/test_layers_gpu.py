@@ -478,3 +478,79 @@ def test_refusals_on_device():
         kda.group_norm_fwd(x, 4, eps=0.0)
     torch.cuda.synchronize()
     assert binding.device_error() == binding.KDA_OK
+
+
+def test_packed_call_without_sequences():
+    """cu_seqlens = [0]: no sequence, no token."""
+    D, S = 8, 4
+    x, bc = torch.zeros(1, 0, D, device="cuda"), torch.zeros(1, 0, 1, S, device="cuda")
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    A, w, k = -torch.ones(D, S, device="cuda"), torch.ones(D, 4, device="cuda"), torch.ones(D, device="cuda")
+    out, fin = kda.ssm_scan_fwd(x, x, A, bc, bc, cu_seqlens=cu)
+    assert out.shape == x.shape and fin.shape == (0, D, S)
+    assert (kda.ssm_scan_bwd(x, x, A, bc, bc, x, cu_seqlens=cu)[2] == 0).all()
+    out, fin = kda.short_conv_fwd(x, w, cu_seqlens=cu)
+    assert fin.shape == (0, 3, D)
+    assert (kda.short_conv_bwd(x, w, x, cu_seqlens=cu)[1] == 0).all()
+    _, mean, rstd = kda.group_norm_fwd(x, 2, k, cu_seqlens=cu)
+    assert mean.shape == (0, 2)
+    assert (kda.group_norm_bwd(x, 2, x, mean, rstd, k, cu_seqlens=cu)[1] == 0).all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_value_stays_in_its_sequence(bad):
+    """The last token of the middle sequence is not finite: the others' rows are
+    bit for bit what they are without it."""
+    g = Gen(19)
+    lengths, D, S = [45, 37, 50], 40, 16
+    x, p = layer_params(g, lengths, D, S, 2, 4, F32)
+    d = g.normal(1, sum(lengths), D)
+
+    def run():
+        h, y, o, mean, rstd = layer(x, p)
+        args = (h, p["delta"], p["A"], p["B"], p["C"])
+        b = kda.ssm_scan_bwd(*args, d, D=p["D"], z=p["z"], delta_bias=p["db"], cu_seqlens=p["cu"], softplus=True)
+        n, m2, r2 = kda.group_norm_fwd(h, 4, p["gw"], p["gb"], cu_seqlens=p["cu"])
+        c = kda.group_norm_bwd(h, 4, d, m2, r2, p["gw"], p["gb"], cu_seqlens=p["cu"])
+        e = kda.short_conv_bwd(x, p["w"], d, p["cb"], None, None, p["cu"], "silu")
+        return [h, y, o, b[0], b[1], b[3], b[4], b[6], n, c[0], e[0]]
+
+    clean = run()
+    x[0, 81, 7] = bad
+    dirty = run()
+    for u, v in zip(clean, dirty):
+        assert torch.equal(u[:, :45], v[:, :45]) and torch.equal(u[:, 82:], v[:, 82:])
+    # a finite state of +-inf inputs is not made NaN by the rows behind the end
+    if bad == float("inf"):
+        _, fin = kda.short_conv_fwd(x, p["w"], None, None, p["cu"])
+        assert fin[1, 2, 7] == float("inf")
+        h = p["delta"].clone()
+        h[0, 81, 7] = bad
+        B = p["B"].abs() + 0.1
+        _, fin = kda.ssm_scan_fwd(h, p["delta"], p["A"], B, p["C"], cu_seqlens=p["cu"], delta_bias=p["db"], softplus=True)
+        assert (fin[1, 7] == float("inf")).all()
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 values a tensor: the last rows are those of a call on them
+    alone."""
+    T, C = 1 << 20, 2176                       # 2.28e9 values, 4.6 GB in bf16
+    x = torch.empty(1, T, C, dtype=BF16, device="cuda")
+    for i in range(0, T, 1 << 16):
+        x[0, i:i + (1 << 16)] = Gen(i).normal(1 << 16, C, dtype=BF16)
+    g, tail = Gen(1), 96
+    w, b = g.normal(C, 4), g.normal(C)
+    out, fin = kda.short_conv_fwd(x, w, b, activation="silu")
+    last = x[:, -tail - 3:].clone()
+    want, _ = kda.short_conv_fwd(last, w, b, activation="silu")
+    assert torch.equal(out[:, -tail:], want[:, -tail:]) and torch.equal(fin[0], x[0, -3:])
+    kda.group_norm_fwd(x, 17, b, b, per_token=True, out=out)
+    want, _, _ = kda.group_norm_fwd(last, 17, b, b, per_token=True)
+    assert torch.equal(out[:, -tail:], want[:, -tail:])
+    # a state that forgets within a few tokens: dt |A| of 8 and more
+    A = torch.full((C, 4), -8.0, device="cuda")
+    bc = g.normal(1, T, 1, 4, dtype=BF16)
+    kda.ssm_scan_fwd(x, x, A, bc, bc, delta_bias=torch.full((C,), 8.0, device="cuda"), softplus=True, out=out)
+    end = bc[:, -tail - 3:].clone()             # a view of these rows is not 16-byte aligned
+    want, _ = kda.ssm_scan_fwd(last, last, A, end, end, delta_bias=torch.full((C,), 8.0, device="cuda"), softplus=True)
+    near(out[0, -tail:], want[0, -tail:].cpu().double(), SCAN_TOL)
