@@ -174,32 +174,45 @@ kda_short_conv_kernel(const T* __restrict__ x, const float* __restrict__ weight,
 }
 
 // One token for each of N sequences: the window state is read, used and
-// shifted by one row in place.
-template <typename T, int W, int V>
+// shifted by one row in place.  A thread takes its channels of R sequences,
+// which share the taps.
+template <typename T, int W, int V, int R>
 __global__ void __launch_bounds__(128)
 kda_short_conv_step_kernel(const T* __restrict__ x, const float* __restrict__ weight,
                            const float* __restrict__ bias, T* state, T* __restrict__ out, int N, int C, int ncb,
                            int act)
 {
     const int c0 = ((int)(blockIdx.x % ncb) * blockDim.x + threadIdx.x) * V;
-    const int n = (int)(blockIdx.x / ncb) * blockDim.y + threadIdx.y;
-    if (c0 >= C || n >= N) return;
-    T* st = state + (size_t)n * (W - 1) * C + c0;
-    float h[W - 1][V], cur[V], v[V];
+    const int n0 = ((int)(blockIdx.x / ncb) * blockDim.y + threadIdx.y) * R;
+    if (c0 >= C || n0 >= N) return;
+    Raw<T, V> rows[R][W];  // the window, then the token
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) load_vec<V>(st + (size_t)j * C, h[j]);
-    load_vec<V>(x + (size_t)n * C + c0, cur);
+    for (int r = 0; r < R; ++r) {
+        const int n = n0 + r < N ? n0 + r : N - 1;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) rows[r][j].load(state + ((size_t)n * (W - 1) + j) * C + c0);
+        rows[r][W - 1].load(x + (size_t)n * C + c0);
+    }
     Taps<W, V> taps;
     taps.load(weight, bias, c0);
-    taps.dot(h, cur, v);
-    if (act) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = silu(v[i]);
+    for (int r = 0; r < R; ++r) {
+        const int n = n0 + r;
+        if (n >= N) break;
+        float h[W - 1][V], cur[V], v[V];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) rows[r][j].get(h[j]);
+        rows[r][W - 1].get(cur);
+        taps.dot(h, cur, v);
+        if (act) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = silu(v[i]);
+        }
+        store_vec<V>(out + (size_t)n * C + c0, v);
+        push<W, V>(h, cur);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) store_vec<V>(state + ((size_t)n * (W - 1) + j) * C + c0, h[j]);
     }
-    store_vec<V>(out + (size_t)n * C + c0, v);
-    push<W, V>(h, cur);
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) store_vec<V>(st + (size_t)j * C, h[j]);
 }
 
 // Backward.  With dv = dy act'(v):
@@ -469,10 +482,13 @@ template <typename T, int W, int V>
 cudaError_t step(const ConvArgs& a, cudaStream_t stream)
 {
     const Shape s = shape_of(a.C, V, 128, 128);
-    const long long blocks = ((long long)a.N + s.ty - 1) / s.ty * s.ncb;
+    // two sequences a thread once that still gives every SM two blocks
+    const int R = (long long)a.N * s.ncb >= 4LL * s.ty * sm_count() ? 2 : 1;
+    const long long blocks = ((long long)a.N + s.ty * R - 1) / (s.ty * R) * s.ncb;
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-    kda_short_conv_step_kernel<T, W, V><<<(unsigned)blocks, dim3(s.tx, s.ty), 0, stream>>>(
-        (const T*)a.x, a.weight, a.bias, (T*)a.final_state, (T*)a.out, a.N, a.C, s.ncb, a.silu);
+    auto* k = R == 2 ? &kda_short_conv_step_kernel<T, W, V, 2> : &kda_short_conv_step_kernel<T, W, V, 1>;
+    k<<<(unsigned)blocks, dim3(s.tx, s.ty), 0, stream>>>((const T*)a.x, a.weight, a.bias, (T*)a.final_state,
+                                                         (T*)a.out, a.N, a.C, s.ncb, a.silu);
     return cudaGetLastError();
 }
 

@@ -554,3 +554,100 @@ def test_offsets_beyond_32_bits():
     end = bc[:, -tail - 3:].clone()             # a view of these rows is not 16-byte aligned
     want, _ = kda.ssm_scan_fwd(last, last, A, end, end, delta_bias=torch.full((C,), 8.0, device="cuda"), softplus=True)
     near(out[0, -tail:], want[0, -tail:].cpu().double(), SCAN_TOL)
+
+
+# ---- sizes that take the paths of large calls -----------------------------------
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_short_conv_large(dtype):
+    """Long runs of tokens per thread, sequence ends inside them."""
+    lengths, C, W = [9001, 1, 0, 6000, 2999], 1024, 4
+    g, T, N = Gen(51), sum(lengths), len(lengths)
+    x, w, b = g.normal(1, T, C, dtype=dtype), g.normal(C, W, std=0.5), g.normal(C)
+    d_out, s0 = g.normal(1, T, C, dtype=dtype), g.normal(N, W - 1, C, dtype=dtype)
+    cu, bounds = cu_of(lengths), ref.bounds_of(lengths)
+    out, fin = kda.short_conv_fwd(x, w, b, s0, cu, "silu")
+    leaves = [wide(x[0]), wide(w), wide(b), wide(s0)]
+    o_ref, f_ref = ref.short_conv(*leaves, bounds, True)
+    near(out[0], o_ref, TOL)
+    assert torch.equal(fin.cpu().double(), f_ref.detach())
+    want = ref.grads_of((o_ref,), (d_out[0].cpu().double(),), leaves)
+    got = kda.short_conv_bwd(x, w, d_out, b, s0, None, cu, "silu")
+    near(got[0][0], want[0], TOL)
+    for u, v in zip(got[1:], want[1:]):
+        near(u, v, 4 * TOL)      # sums over 18001 tokens
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("W", [2, 3, 4])
+def test_short_conv_step_large(dtype, W):
+    """Two sequences a thread, the last one alone."""
+    N, C = 1201, 1024
+    g = Gen(52)
+    x, w, b, st = g.normal(N, C, dtype=dtype), g.normal(C, W), g.normal(C), g.normal(N, W - 1, C, dtype=dtype)
+    want, fin = kda.short_conv_fwd(x[:, None].contiguous(), w, b, st, activation="silu")
+    assert torch.equal(kda.short_conv_step(x, w, st, b, "silu"), want[:, 0])
+    assert torch.equal(st, fin)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("S,G", [(16, 2), (13, 1), (40, 1)])
+def test_ssm_step_large(dtype, S, G):
+    """Four sequences a thread, three for the last."""
+    N, D = 4791, 64
+    g = Gen(53)
+    (u, d, A, B, C), opt = scan_inputs(g, (N, 1), D, S, G, dtype)
+    st = g.normal(N, D, S)
+    h, (dt, x) = st.double(), (torch.nn.functional.softplus(d[:, 0].double() + opt["delta_bias"]), u[:, 0].double())
+    Bd, Cd = (m[:, 0].double().repeat_interleave(D // G, 1) for m in (B, C))
+    h = torch.exp(dt[..., None] * A) * h + (dt * x)[..., None] * Bd
+    y = (h * Cd).sum(-1) + opt["D"] * x
+    z = opt["z"][:, 0].double()
+    out = kda.ssm_step(u[:, 0], d[:, 0], A, B[:, 0], C[:, 0], st, D=opt["D"], z=opt["z"][:, 0],
+                       delta_bias=opt["delta_bias"], softplus=True)
+    near(out, (y * z * torch.sigmoid(z)).cpu(), TOL)
+    near(st, h.cpu(), TOL)
+
+
+@pytest.mark.parametrize("lengths", [None, [130, 40, 3, 100]])
+def test_ssm_scan_many_chains(lengths):
+    """Chains enough that sequences of one length stay whole, and ragged ones
+    are cut at the mean."""
+    D, S = 4096, 16
+    g = Gen(54)
+    lead = (4, 70) if lengths is None else (1, sum(lengths))
+    assert (kda.ssm_scan_fwd_workspace_bytes(*lead, D, S, 1, 4, lengths is not None, BF16) == 0) == (lengths is None)
+    args, opt = scan_inputs(g, lead, D, S, 1, BF16)
+    bounds = ref.bounds_of(lengths or [70] * 4)
+    check_scan(lead, bounds, cu_of(lengths) if lengths else None, args, opt, g.normal(4, D, S),
+               g.normal(*lead, D, dtype=BF16), g.normal(4, D, S))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("C,groups", [(256, 2), (72, 9), (1536, 1)])
+@pytest.mark.parametrize("per_token", [True, False])
+def test_group_norm_large(dtype, C, groups, per_token):
+    """More rows than walkers, more tokens than a unit."""
+    lengths = [7001, 0, 12000, 999]
+    g, T = Gen(55), sum(lengths)
+    x = (g.normal(1, T, C) + g.normal(C)).to(dtype)
+    w, b, d_out = 1 + g.normal(C, std=0.2), g.normal(C), g.normal(1, T, C, dtype=dtype)
+    cu = cu_of(lengths)
+    out, mean, rstd = kda.group_norm_fwd(x, groups, w, b, 1e-5, "silu", per_token, cu)
+    xs, ws, bs = wide(x[0]), wide(w), wide(b)
+    if per_token:
+        r = xs.view(T, groups, -1)
+        m = r.mean(-1)
+        rs = ((r - m[..., None]).square().mean(-1) + 1e-5).rsqrt()
+        v = ((r - m[..., None]) * rs[..., None]).reshape(T, C) * ws + bs
+        o_ref, m_ref, r_ref = v * torch.sigmoid(v), m, rs
+    else:
+        o_ref, m_ref, r_ref = ref.group_norm(xs, groups, ws, bs, 1e-5, ref.bounds_of(lengths), True)
+    near(out[0], o_ref, TOL)
+    near(mean, m_ref, 2 * TOL)   # means near zero of values near one
+    near(rstd, r_ref, TOL)
+    dx, dw, db = kda.group_norm_bwd(x, groups, d_out, mean, rstd, w, b, "silu", per_token, cu)
+    want = ref.grads_of((o_ref,), (d_out[0].cpu().double(),), [xs, ws, bs])
+    near(dx[0], want[0], 4 * TOL)
+    near(dw, want[1], 4 * TOL)   # sums over 20000 tokens
+    near(db, want[2], 4 * TOL)
