@@ -7,10 +7,17 @@
 // output) or a whole sequence.
 //
 // Per token, a row of one group is contiguous and fits the registers of a few
-// lanes: one read, one write (memory-bound).  Over sequences, three launches:
-// partial statistics of units of tokens, their combination in a fixed order,
-// and the normalisation (x is read twice; what fits the 126 MB L2 comes from
-// HBM once).
+// lanes: one read, one write (memory-bound).  16384 x 4096 in bf16, 32 groups,
+// SiLU: 70 us, 3.9 TB/s (60 % of the measured copy rate); instructions (64 % of
+// the slots) and the SiLU's two special functions (51 %) are as near their limits.
+// Two rows at a time in 64 registers and four blocks an SM; four rows in 103
+// registers and two blocks took 98 us.
+//
+// Over sequences, three launches: partial statistics of units of tokens, their
+// combination in a fixed order, and the normalisation (x is read twice; what
+// fits the 126 MB L2 comes from HBM once).  24007 x 640 in 11 sequences, forward
+// and backward: 100 us in six launches, against 28 us for its bytes: each launch
+// is a few microseconds of finding its unit, latency and its own ramp.
 //
 // Sums of squares run over deviations: within a thread from the thread's first
 // value, across threads and units from the common mean,

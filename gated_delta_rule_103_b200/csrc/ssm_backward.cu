@@ -18,6 +18,14 @@
 // Where sequences are cut into units, a pass before it gives every unit its
 // end state from zero, its sum of dt, and the adjoint it hands to the unit in
 // front, sum_t (prod_{s <= t} a_s) C_t dy_t, all in one walk.
+//
+// 4 x 1024 tokens of 4096 channels, 16 states, bf16: 471 us for the walk back,
+// 106 us for the entry states, 14 us for the sums; their exponentials alone are
+// some 250 us of the special function unit.  The walk back takes 240 instructions
+// a warp, token and 16 channels (states again 56, adjoints and their sums 90,
+// folds 46) at two warps a scheduler, which fill half of the issue slots.  A lane
+// per channel and 4 states, in packed arithmetic, took 650 us: twice the folds,
+// and the reads of B and C.
 #include "ssm_common.cuh"
 
 namespace kda {
@@ -567,8 +575,10 @@ kda_ssm_bwd_sums_kernel(const float* __restrict__ part_bc, float* __restrict__ g
     }
 }
 
-// Sequences are cut where the chains give the SMs fewer warps than this: two
-// more walks then go over most tokens, a third of the whole.
+// Sequences are cut where the chains give the SMs fewer warps than this: another
+// walk then goes over most tokens, a fifth of the whole.  (4 x 1024 x 4096, 6.9
+// warps an SM: 757 us whole, 916 us cut; units for 16 warps of at least 32 tokens
+// against 8 and 64: 17245 x 640 628 against 676 us, small calls 5 to 20 % less.)
 constexpr int kBwdFewWarps = 5, kBwdWantWarps = 16, kBwdShortest = 32;
 
 struct Layout {
