@@ -590,7 +590,7 @@ Layout layout_of(int B, int T, int D, int S, int G, int N, int packed)
 {
     Layout l = {};
     const size_t tokens = (size_t)B * T, DS = (size_t)D * S, L = lanes_of(S);
-    l.c = cut_of(B, T, N, packed, (double)D * L / 64.0, kBwdFewWarps, kBwdWantWarps, kBwdShortest);
+    l.c = cut_of(B, T, N, packed, (double)D * L / 64.0, kBwdFewWarps, kBwdWantWarps, kBwdShortest, 2 * kBwdShortest);
     l.slots = (size_t)slots_of(B, T, N, packed, l.c.len);
     const size_t CH = 256 / L, cpb = ((size_t)(D / G) + CH - 1) / CH, TT = L >= 4 ? 16 : 4 * L;  // as in Bwd<L>
     l.tiles = tokens / TT + l.slots + 1;

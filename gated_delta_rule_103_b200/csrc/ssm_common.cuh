@@ -365,12 +365,12 @@ struct Cut {
 };
 // Cut only where the chains (chain_warps warps a sequence) give the SMs under
 // `few` warps each, then into units that give them `want`; no unit is shorter
-// than `shortest` tokens.
-inline Cut cut_of(int B, int T, int N, int packed, double chain_warps, int few, int want, int shortest)
+// than `shortest` tokens, and no call of fewer than `least` is cut.
+inline Cut cut_of(int B, int T, int N, int packed, double chain_warps, int few, int want, int shortest, int least)
 {
     Cut c = {T > 0 ? (T + 15) / 16 * 16 : 16, false};
     const long long tokens = (long long)B * T;
-    if (tokens == 0 || N == 0) return c;
+    if (tokens == 0 || N == 0 || T < least) return c;
     const bool many = (double)sm_count() * few <= chain_warps * N;
     if (many && !packed) return c;
     const double units = (double)sm_count() * want / chain_warps;

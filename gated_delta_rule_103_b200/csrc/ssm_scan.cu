@@ -364,12 +364,13 @@ kda_ssm_step_kernel(const T* __restrict__ u, const T* __restrict__ delta, const 
 // A unit's tokens are passed over twice where sequences are cut, which pays where
 // the SMs have under six warps each (3.5 warps: 930 us whole, 533 us cut; 6.9
 // warps: 529 us whole, 1088 us cut), and then into units for sixteen warps each
-// (20011 tokens of 1100 channels: 283 us, 348 us for twelve).
-constexpr int kFewWarps = 6, kWantWarps = 16, kShortest = 32;
+// (20011 tokens of 1100 channels: 283 us, 348 us for twelve).  The two launches
+// more are worth some hundred tokens.
+constexpr int kFewWarps = 6, kWantWarps = 16, kShortest = 32, kLeast = 128;
 
 Cut fwd_cut(int B, int T, int D, int S, int N, int packed)
 {
-    return cut_of(B, T, N, packed, (double)D * lanes_of(S) / 64.0, kFewWarps, kWantWarps, kShortest);
+    return cut_of(B, T, N, packed, (double)D * lanes_of(S) / 64.0, kFewWarps, kWantWarps, kShortest, kLeast);
 }
 
 template <typename T, int L>

@@ -89,6 +89,13 @@ class _On:
             self.context.__exit__(*error)
 
 
+def _out(x: torch.Tensor, stream) -> torch.Tensor:
+    if stream is None:
+        return torch.empty_like(x)
+    with _On(stream):
+        return torch.empty_like(x)
+
+
 def _raw(stream, t: torch.Tensor) -> int:
     """The stream's handle: the given one, or the current one of t's device
     (the library refuses tensors of another device than the current one)."""
@@ -178,14 +185,13 @@ def short_conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor,
     flags = _activation(activation)
     px, pw = _take(x, "x", x.shape, dtype), _take(weight, "weight", (C, W), _F32)
     pb, ps = _take(bias, "bias", (C,), _F32), _take(state, "state", (N, W - 1, C), dtype)
-    if out is None:
-        if stream is None:
-            out = torch.empty_like(x)
-        else:
-            with _On(stream):
-                out = torch.empty_like(x)
-    _check(lib.kda_short_conv_step(px, pw, pb, ps, _take(out, "out", x.shape, dtype), N, C, W, dt,
-                                   flags, _raw(stream, x)), "kda_short_conv_step")
+    if out is not None:
+        po = _take(out, "out", x.shape, dtype)
+    else:
+        out = _out(x, stream)
+        po = out.data_ptr()
+    _check(lib.kda_short_conv_step(px, pw, pb, ps, po, N, C, W, dt, flags, _raw(stream, x)),
+           "kda_short_conv_step")
     return out
 
 
@@ -257,16 +263,16 @@ def ssm_scan_bwd_workspace_bytes(B: int, T: int, D: int, S: int, G: int, N: int,
 
 def _scan_inputs(u, delta, A, B, C, D, z, delta_bias, lead: int):
     """Addresses of the scan's inputs, checked against u's leading dimensions."""
-    shape = _rank(u, "u", lead + 1)
-    dtype = u.dtype
+    shape, dtype = u.shape, u.dtype
     ch = shape[-1]
     S = _rank(A, "A", 2)[1]
     bc = _rank(B, "B", lead + 2)
-    if bc[:lead] != shape[:lead] or bc[-1] != S or bc[-2] < 1 or ch % bc[-2]:
+    G = bc[lead]
+    if bc != (*shape[:lead], G, S) or G < 1 or ch % G:
         raise ValueError("B must be [..., G, S] with u's leading dimensions, A's S and G dividing the channels")
     return (_take(u, "u", shape, dtype), _take(delta, "delta", shape, dtype), _take(A, "A", (ch, S), _F32),
             _take(B, "B", bc, dtype), _take(C, "C", bc, dtype), _take(D, "D", (ch,), _F32),
-            _take(z, "z", shape, dtype), _take(delta_bias, "delta_bias", (ch,), _F32)), ch, S, bc[-2]
+            _take(z, "z", shape, dtype), _take(delta_bias, "delta_bias", (ch,), _F32)), ch, S, G
 
 
 def ssm_scan_fwd(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
@@ -319,18 +325,17 @@ def ssm_step(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch.Ten
     u, delta, z [N,channels], B, C [N,G,S]; ``state`` [N,channels,S] fp32 is
     updated in place.  Returns out [N,channels]."""
     lib = load_library()
+    N, _ = _rank(u, "u", 2)
     dt = _dtype(u, "u")
     ins, ch, S, G = _scan_inputs(u, delta, A, B, C, D, z, delta_bias, 1)
-    N = u.shape[0]
     ps = _take(state, "state", (N, ch, S), _F32)
-    if out is None:
-        if stream is None:
-            out = torch.empty_like(u)
-        else:
-            with _On(stream):
-                out = torch.empty_like(u)
-    _check(lib.kda_ssm_step(*ins, ps, _take(out, "out", u.shape, u.dtype), N, ch, S, G, dt,
-                            KDA_FLAG_SOFTPLUS if softplus else 0, _raw(stream, u)), "kda_ssm_step")
+    if out is not None:
+        po = _take(out, "out", u.shape, u.dtype)
+    else:
+        out = _out(u, stream)
+        po = out.data_ptr()
+    _check(lib.kda_ssm_step(*ins, ps, po, N, ch, S, G, dt, KDA_FLAG_SOFTPLUS if softplus else 0,
+                            _raw(stream, u)), "kda_ssm_step")
     return out
 
 

@@ -651,3 +651,77 @@ def test_group_norm_large(dtype, C, groups, per_token):
     near(dx[0], want[0], 4 * TOL)
     near(dw, want[1], 4 * TOL)   # sums over 20000 tokens
     near(db, want[2], 4 * TOL)
+
+
+def test_calls_with_every_buffer_given_allocate_nothing():
+    """Outputs, states, gradients and workspaces of the caller: the results are
+    the same, and neither the library nor the binding takes device memory."""
+    g = Gen(61)
+    lengths, D, S, groups = [300, 170], 96, 16, 4
+    T, N = sum(lengths), len(lengths)
+    x, p = layer_params(g, lengths, D, S, 2, groups, BF16)
+    d = g.normal(1, T, D, dtype=BF16)
+    args = (x, p["delta"], p["A"], p["B"], p["C"])
+    opt = dict(D=p["D"], z=p["z"], delta_bias=p["db"], cu_seqlens=p["cu"], softplus=True)
+
+    def f32(*shape):
+        return torch.empty(shape, device="cuda")
+
+    def space(n):
+        assert n > 0
+        return torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+
+    out, conv_state, scan_state = torch.empty_like(x), torch.empty(N, 3, D, dtype=BF16, device="cuda"), f32(N, D, S)
+    norm = (torch.empty_like(x), f32(N, groups), f32(N, groups))
+    conv_grads = (f32(1, T, D), f32(D, 4), f32(D), f32(N, 3, D))
+    scan_grads = (f32(1, T, D), f32(1, T, D), f32(D, S), f32(1, T, 2, S), f32(1, T, 2, S), f32(D), f32(1, T, D), f32(D),
+                  f32(N, D, S))
+    norm_grads = (f32(1, T, D), f32(D), f32(D))
+    ws = [space(kda.ssm_scan_fwd_workspace_bytes(1, T, D, S, 2, N, True)),
+          space(kda.ssm_scan_bwd_workspace_bytes(1, T, D, S, 2, N, True)),
+          space(kda.short_conv_bwd_workspace_bytes(1, T, D, 4, N, True)),
+          space(kda.group_norm_workspace_bytes(1, T, D, groups, N, True)),
+          space(kda.group_norm_workspace_bytes(1, T, D, groups, N, True, backward=True))]
+
+    def step():
+        kda.short_conv_fwd(x, p["w"], p["cb"], None, p["cu"], "silu", out=out, final_state=conv_state)
+        kda.short_conv_bwd(x, p["w"], d, p["cb"], None, None, p["cu"], "silu", grads=conv_grads, workspace=ws[2])
+        kda.ssm_scan_fwd(*args, **opt, out=out, final_state=scan_state, workspace=ws[0])
+        kda.ssm_scan_bwd(*args, d, **opt, grads=scan_grads, workspace=ws[1])
+        kda.group_norm_fwd(x, groups, p["gw"], p["gb"], cu_seqlens=p["cu"], out=norm[0], mean=norm[1], rstd=norm[2],
+                           workspace=ws[3])
+        kda.group_norm_bwd(x, groups, d, norm[1], norm[2], p["gw"], p["gb"], cu_seqlens=p["cu"], grads=norm_grads,
+                           workspace=ws[4])
+
+    step()
+    torch.cuda.synchronize()
+    free, held = torch.cuda.mem_get_info()[0], torch.cuda.memory_allocated()
+    for _ in range(2):
+        step()
+    torch.cuda.synchronize()
+    assert torch.cuda.mem_get_info()[0] == free and torch.cuda.memory_allocated() == held
+    y, st = kda.ssm_scan_fwd(*args, **opt)
+    assert torch.equal(out, y) and torch.equal(scan_state, st)
+    for u, v in zip(scan_grads, kda.ssm_scan_bwd(*args, d, **opt)):
+        assert torch.equal(u, v)
+    for u, v in zip(norm_grads, kda.group_norm_bwd(x, groups, d, norm[1], norm[2], p["gw"], p["gb"], cu_seqlens=p["cu"])):
+        assert torch.equal(u, v)
+    for u, v in zip(conv_grads, kda.short_conv_bwd(x, p["w"], d, p["cb"], None, None, p["cu"], "silu")):
+        assert torch.equal(u, v)
+
+
+def test_workspaces_that_do_not_fit_are_refused():
+    g = Gen(62)
+    args, opt = scan_inputs(g, (1, 300), 32, 16, 1, F32)
+    need = kda.ssm_scan_fwd_workspace_bytes(1, 300, 32, 16, 1, 1, False, F32)
+    assert need > 0
+    ws = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="workspace"):
+        kda.ssm_scan_fwd(*args, **opt, workspace=ws[:need - 1])
+    with pytest.raises(binding.KDAError):             # not 256-byte aligned
+        kda.ssm_scan_fwd(*args, **opt, workspace=ws[16:])
+    big = torch.empty((1, 300, 32), device="cuda")
+    with pytest.raises(binding.KDAError):             # the output's memory
+        kda.ssm_scan_fwd(*args, **opt, out=big, workspace=torch.as_strided(
+            big.view(torch.uint8), (max(need, 1),), (1,)) if need <= big.numel() * 4 else ws[16:])
+    kda.ssm_scan_fwd(*args, **opt, workspace=ws)
