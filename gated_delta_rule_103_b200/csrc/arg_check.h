@@ -11,8 +11,8 @@
 namespace kda {
 
 // A pointer the kernels may dereference: device (or managed) memory of the
-// current device, 16-byte aligned.
-inline bool device_ptr_ok(const void* p)
+// current device `dev`, 16-byte aligned.
+inline bool device_ptr_ok(const void* p, int dev)
 {
     if (!p) return false;
     if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return false;
@@ -22,9 +22,13 @@ inline bool device_ptr_ok(const void* p)
         return false;
     }
     if (attr.type != cudaMemoryTypeDevice && attr.type != cudaMemoryTypeManaged) return false;
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
     return attr.type == cudaMemoryTypeManaged || attr.device == dev;
+}
+
+inline bool device_ptr_ok(const void* p)
+{
+    int dev = -1;
+    return p && cudaGetDevice(&dev) == cudaSuccess && device_ptr_ok(p, dev);
 }
 
 inline bool overlaps(const void* a, size_t na, const void* b, size_t nb)

@@ -44,13 +44,14 @@ private:
     {
         if (!p && (optional || n == 0)) return;
         if (n == 0) return;  // nothing is read or written there
-        if (!device_ptr_ok(p)) ok_ = false;
+        if (dev_ < 0 && cudaGetDevice(&dev_) != cudaSuccess) ok_ = false;
+        if (!device_ptr_ok(p, dev_)) ok_ = false;
         r_[n_] = {p, n};
         written_[n_++] = written;
     }
     Region r_[24];
     bool written_[24];
-    int n_ = 0;
+    int n_ = 0, dev_ = -1;
     bool ok_ = true;
 };
 

@@ -225,11 +225,15 @@ struct Units {
     }
 };
 
+// SMs of the current device.
 inline int sm_count()
 {
+    static int known[64] = {};  // a device's count does not change: any thread writes the same
     int dev = 0, sms = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess)
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (cudaGetDevice(&dev) != cudaSuccess) return sms;
+    if (dev >= 0 && dev < 64 && known[dev]) return known[dev];
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (dev >= 0 && dev < 64) known[dev] = sms;
     return sms;
 }
 
