@@ -51,13 +51,18 @@ __device__ __forceinline__ float part_sum(float v, int lanes)
 // values (l + i LANES) V; kFull: they are Cg to the last one).  A lane keeps to
 // one group, so that its weights stay in registers while it walks the tokens, U
 // at a time: their loads are in flight and their sums are folded together.
-constexpr int rows_blocks(int nv, bool full, bool bwd)  // per SM
+// By the values a lane holds of a row: blocks per SM, and rows at a time.
+constexpr int rows_blocks(int values, bool full, bool bwd)
 {
-    return bwd ? (nv == 1 ? 2 : 1) : (nv == 1 ? (full ? 4 : 3) : 2);
+    return bwd ? (values <= 4 ? 3 : values <= 8 ? 2 : 1) : (values <= 8 ? (full ? 4 : 3) : 2);
+}
+constexpr int rows_at_once(int values, bool bwd)
+{
+    return values <= 2 || (values <= 4 && !bwd) ? 4 : values <= 8 ? 2 : 1;
 }
 
 template <typename T, int V, int LANES, int NV, bool kFull, bool kBwd>
-__global__ void __launch_bounds__(256, rows_blocks(NV, kFull, kBwd))
+__global__ void __launch_bounds__(256, rows_blocks(V * NV, kFull, kBwd))
 kda_norm_rows_kernel(const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
                      T* __restrict__ out, float* __restrict__ mean, float* __restrict__ rstd,
                      const T* __restrict__ d_out, float* __restrict__ grad_x, float* __restrict__ part,
@@ -81,7 +86,7 @@ kda_norm_rows_kernel(const T* __restrict__ x, const float* __restrict__ weight, 
             if (kBwd) dw[kBwd ? i : 0][j] = db[kBwd ? i : 0][j] = 0.f;
         }
     const float inv = 1.f / (float)Cg;
-    constexpr int U = NV == 1 ? 2 : 1;
+    constexpr int U = rows_at_once(V * NV, kBwd);
     const int steps = (rows + walkers - 1) / walkers;
     for (int s = 0; s < steps; s += U) {
         size_t at[U];
@@ -212,8 +217,7 @@ __device__ __forceinline__ float block_sum(float v, float* red)
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s += red[i];
+    for (int i = 0; i < (int)blockDim.x / 32; ++i) s += red[i];
     return s;
 }
 
@@ -373,7 +377,7 @@ kda_norm_stats_kernel(const T* __restrict__ x, float* __restrict__ part, Units u
     float cnt = 0.f, mean = 0.f, dev = 0.f;
     if (ty < l.ty && a + ty < b) {
         const float rows = (float)((b - a - ty + l.ty - 1) / l.ty * V);
-        for (int c = cx; c < groups * l.cpg; c += wide ? 256 : l.cols) {
+        for (int c = cx; c < groups * l.cpg; c += wide ? l.threads : l.cols) {
             const T* p = x + ((size_t)g0 * l.cpg + c) * V;
             float first[V], s1 = 0.f, s2 = 0.f;
             load_vec<V>(p + (size_t)(a + ty) * C, first);
@@ -399,7 +403,7 @@ kda_norm_stats_kernel(const T* __restrict__ x, float* __restrict__ part, Units u
     sq[threadIdx.x] = dev;
     __syncthreads();
     // over a group's threads, `lg` lanes a group: all groups at once where they fit
-    const int per = wide ? 256 : l.cpg * l.ty;
+    const int per = wide ? l.threads : l.cpg * l.ty;
     int lg = 32;
     while (lg > 1 && (lg / 2 >= per || lg * groups > l.threads)) lg >>= 1;
     const int sub = threadIdx.x % lg, across = l.threads / lg;
@@ -494,7 +498,7 @@ kda_norm_apply_kernel(const T* __restrict__ x, const float* __restrict__ weight,
     const int ty = wide ? 0 : threadIdx.x / l.cols;
     const int cx = wide ? threadIdx.x : threadIdx.x % l.cols;
     if (ty >= l.ty) return;
-    for (int c = cx; c < groups * l.cpg; c += wide ? 256 : l.cols) {
+    for (int c = cx; c < groups * l.cpg; c += wide ? l.threads : l.cols) {
         const int ch = (g0 * l.cpg + c) * V;
         const size_t ng = (size_t)n * G + g0 + c / l.cpg;
         const float m = mean[ng], rs = rstd[ng];
@@ -556,7 +560,7 @@ kda_norm_bwd_sums_kernel(const T* __restrict__ x, const float* __restrict__ weig
     const int ty = wide ? 0 : threadIdx.x / l.cols;
     const int cx = wide ? threadIdx.x : threadIdx.x % l.cols;
     float s1 = 0.f, s2 = 0.f;
-    for (int c = cx; c < groups * l.cpg; c += wide ? 256 : l.cols) {
+    for (int c = cx; c < groups * l.cpg; c += wide ? l.threads : l.cols) {
         if (ty >= l.ty) break;
         const int ch = ch0 + c * V;
         const size_t ng = (size_t)n * G + g0 + c / l.cpg;
@@ -707,7 +711,8 @@ Layout layout_of(int C, int G, int V, long long tokens)
         l.gb = 1;
         l.cols = l.cpg;
         l.ty = 1;
-        l.threads = 256;
+        const int rounds = (l.cpg + 255) / 256;  // columns of a thread
+        l.threads = ((l.cpg + rounds - 1) / rounds + 31) / 32 * 32;
     } else {
         l.gb = 256 / l.cpg < G ? 256 / l.cpg : G;
         l.cols = l.gb * l.cpg;
@@ -755,7 +760,7 @@ RowShape row_shape(long long rows, int C, int G, kda_dtype dtype, bool bwd)
     const int per_block = r.nv <= 4 ? 256 / r.lanes : 1;  // rows in flight
     if (r.nv > 4) r.lanes = r.nv = 0;
     // as many walkers as the SMs hold at a time, none without a row
-    const long long want = (long long)sm_count() * (r.nv ? rows_blocks(r.nv, r.lanes * r.nv * r.V == Cg, bwd) : 4) * per_block;
+    const long long want = (long long)sm_count() * (r.nv ? rows_blocks(r.V * r.nv, r.lanes * r.nv * r.V == Cg, bwd) : 4) * per_block;
     long long w = (want + G - 1) / G;
     if (w > rows) w = rows;
     if (w < 1) w = 1;
