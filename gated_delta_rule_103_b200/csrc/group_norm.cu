@@ -46,8 +46,30 @@ __device__ __forceinline__ float part_sum(float v, int lanes)
     return v;
 }
 
+// Sums over a row's LANES lanes of each of v: lanes of a warp, or all 256 threads
+// of the block (red: theirs to use; every thread of the block takes part).
+template <int LANES, int U>
+__device__ __forceinline__ void row_sums(float (&v)[U], float (*red)[8])
+{
+#pragma unroll
+    for (int q = 0; q < U; ++q) v[q] = lane_sum<(LANES < 32 ? LANES : 32)>(v[q]);
+    if constexpr (LANES > 32) {
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int q = 0; q < U; ++q) red[q][threadIdx.x >> 5] = v[q];
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            v[q] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[q] += red[q][i];
+        }
+    }
+}
+
 // ---- per token --------------------------------------------------------------
-// LANES lanes hold one row of Cg = C / G values, NV vectors of V each (lane l:
+// LANES lanes (up to a warp, or the block's 256 threads) hold one row of Cg = C / G values, NV vectors of V each (lane l:
 // values (l + i LANES) V; kFull: they are Cg to the last one).  A lane keeps to
 // one group, so that its weights stay in registers while it walks the tokens, U
 // at a time: their loads are in flight and their sums are folded together.
@@ -87,6 +109,7 @@ kda_norm_rows_kernel(const T* __restrict__ x, const float* __restrict__ weight, 
         }
     const float inv = 1.f / (float)Cg;
     constexpr int U = rows_at_once(V * NV, kBwd);
+    __shared__ float red[LANES > 32 ? U : 1][8];
     const int steps = (rows + walkers - 1) / walkers;
     for (int s = 0; s < steps; s += U) {
         size_t at[U];
@@ -128,8 +151,10 @@ kda_norm_rows_kernel(const T* __restrict__ x, const float* __restrict__ weight, 
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
                     for (int j = 0; j < V; ++j) s1[q] += v[q][i][j];
-                m[q] = lane_sum<LANES>(s1[q]) * inv;
             }
+            row_sums<LANES>(s1, red);
+#pragma unroll
+            for (int q = 0; q < U; ++q) m[q] = s1[q] * inv;
 #pragma unroll
             for (int q = 0; q < U; ++q) {
 #pragma unroll
@@ -140,8 +165,10 @@ kda_norm_rows_kernel(const T* __restrict__ x, const float* __restrict__ weight, 
                             const float d = v[q][i][j] - m[q];
                             s2[q] = fmaf(d, d, s2[q]);
                         }
-                rs[q] = 1.f / sqrtf(fmaf(lane_sum<LANES>(s2[q]), inv, eps));
             }
+            row_sums<LANES>(s2, red);
+#pragma unroll
+            for (int q = 0; q < U; ++q) rs[q] = 1.f / sqrtf(fmaf(s2[q], inv, eps));
 #pragma unroll
             for (int q = 0; q < U; ++q) {
                 if (!here[q]) continue;
@@ -183,11 +210,13 @@ kda_norm_rows_kernel(const T* __restrict__ x, const float* __restrict__ weight, 
                         s2[q] = fmaf(d, xh, s2[q]);
                     }
                 }
-                s1[q] = lane_sum<LANES>(s1[q]) * inv;
-                s2[q] = lane_sum<LANES>(s2[q]) * inv;
             }
+            row_sums<LANES>(s1, red);
+            row_sums<LANES>(s2, red);
 #pragma unroll
             for (int q = 0; q < U; ++q) {
+                s1[q] *= inv;
+                s2[q] *= inv;
                 if (!here[q]) continue;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
@@ -221,7 +250,7 @@ __device__ __forceinline__ float block_sum(float v, float* red)
     return s;
 }
 
-// Rows too long for a warp's registers: a block per (walker, group), the row
+// Rows too long for a block's registers: a block per (walker, group), the row
 // read again from L1/L2 for each pass.  The parameters' sums stay in the
 // block's own rows of `part`, where only this thread adds to them.
 template <typename T, int V, bool kBwd>
@@ -755,6 +784,7 @@ RowShape row_shape(long long rows, int C, int G, kda_dtype dtype, bool bwd)
     const int vecs = Cg / r.V;
     r.lanes = 1;
     while (r.lanes < 32 && r.lanes < vecs) r.lanes <<= 1;
+    if (vecs > 4 * 32) r.lanes = 256;  // more than a warp holds
     r.nv = 1;
     while (r.nv * r.lanes < vecs) r.nv <<= 1;
     const int per_block = r.nv <= 4 ? 256 / r.lanes : 1;  // rows in flight
@@ -805,6 +835,7 @@ cudaError_t rows(const NormArgs& a, const RowShape& r, cudaStream_t st)
         case 8: return rows_nv<T, V, 8, kBwd>(a, r, st);
         case 16: return rows_nv<T, V, 16, kBwd>(a, r, st);
         case 32: return rows_nv<T, V, 32, kBwd>(a, r, st);
+        case 256: return rows_nv<T, V, 256, kBwd>(a, r, st);
     }
     kda_norm_long_rows_kernel<T, V, kBwd><<<(unsigned)r.blocks, 256, 0, st>>>(
         (const T*)a.x, a.weight, a.bias, (T*)a.out, a.mean, a.rstd, (const T*)a.d_out, a.grad_x,
