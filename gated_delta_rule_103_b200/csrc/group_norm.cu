@@ -7,7 +7,7 @@
 // output) or a whole sequence.
 //
 // Per token, a row of one group is contiguous and fits the registers of a few
-// lanes: one read, one write (memory-bound).  16384 x 4096 in bf16, 32 groups,
+// lanes, at most a block's: one read, one write (memory-bound).  16384 x 4096 in bf16, 32 groups,
 // SiLU: 70 us, 3.9 TB/s (60 % of the measured copy rate); instructions (64 % of
 // the slots) and the SiLU's two special functions (51 %) are as near their limits.
 // Two rows at a time in 64 registers and four blocks an SM; four rows in 103
@@ -82,6 +82,13 @@ constexpr int rows_at_once(int values, bool bwd)
 {
     return values <= 2 || (values <= 4 && !bwd) ? 4 : values <= 8 ? 2 : 1;
 }
+// Vectors of a row that a lane holds at most: 16 values in a warp's lane (32 in
+// vectors of 8), then the row takes the block; 32 in a block's, 16 in vectors of
+// one.  Forward and backward, SiLU, bf16: 3191 x 4640 in 32 groups (of 145: 5
+// values a lane) 107 us in a warp, 435 in a block; 4096 x 8190 in one group 179 in
+// a block, 360 reading the row again; but 8192 x 4097 923 in a block of 32 values a
+// lane, 298 reading it again.
+constexpr int most_vectors(int V, int lanes) { return V > 1 && (lanes > 32 || V > 4) ? 32 / V : 16 / V; }
 
 template <typename T, int V, int LANES, int NV, bool kFull, bool kBwd>
 __global__ void __launch_bounds__(256, rows_blocks(V * NV, kFull, kBwd))
@@ -784,11 +791,12 @@ RowShape row_shape(long long rows, int C, int G, kda_dtype dtype, bool bwd)
     const int vecs = Cg / r.V;
     r.lanes = 1;
     while (r.lanes < 32 && r.lanes < vecs) r.lanes <<= 1;
-    if (vecs > 4 * 32) r.lanes = 256;  // more than a warp holds
+    if (vecs > 32 * most_vectors(r.V, 32)) r.lanes = 256;
     r.nv = 1;
     while (r.nv * r.lanes < vecs) r.nv <<= 1;
-    const int per_block = r.nv <= 4 ? 256 / r.lanes : 1;  // rows in flight
-    if (r.nv > 4) r.lanes = r.nv = 0;
+    const bool fits = r.nv <= most_vectors(r.V, r.lanes);
+    const int per_block = fits ? 256 / r.lanes : 1;  // rows in flight
+    if (!fits) r.lanes = r.nv = 0;
     // as many walkers as the SMs hold at a time, none without a row
     const long long want = (long long)sm_count() * (r.nv ? rows_blocks(r.V * r.nv, r.lanes * r.nv * r.V == Cg, bwd) : 4) * per_block;
     long long w = (want + G - 1) / G;
@@ -803,6 +811,8 @@ template <typename T, int V, int LANES, bool kBwd>
 cudaError_t rows_nv(const NormArgs& a, const RowShape& r, cudaStream_t st)
 {
     const int rows = a.B * a.T;
+    // a power of two of lanes and vectors fills a row with the widest vectors only
+    constexpr bool kWhole = LANES == 1 || V == 16 / (int)sizeof(T);
     const bool full = r.lanes * r.nv * V == a.C / a.G;
 #define KDA_NORM_ROWS_OF(NV, FULL)                                                                             \
     kda_norm_rows_kernel<T, V, LANES, NV, FULL, kBwd><<<(unsigned)r.blocks, 256, 0, st>>>(                     \
@@ -810,19 +820,27 @@ cudaError_t rows_nv(const NormArgs& a, const RowShape& r, cudaStream_t st)
         (float*)a.workspace, rows, a.G, a.C / a.G, r.walkers, a.eps, a.silu)
 #define KDA_NORM_ROWS(NV)                                                                                      \
     do {                                                                                                       \
-        if (full) KDA_NORM_ROWS_OF(NV, true);                                                                  \
-        else KDA_NORM_ROWS_OF(NV, false);                                                                      \
+        if constexpr (kWhole) {                                                                                \
+            if (full) KDA_NORM_ROWS_OF(NV, true);                                                              \
+            else KDA_NORM_ROWS_OF(NV, false);                                                                  \
+        } else {                                                                                               \
+            KDA_NORM_ROWS_OF(NV, false);                                                                       \
+        }                                                                                                      \
+        return cudaGetLastError();                                                                             \
     } while (0)
-    if constexpr (LANES < 32) {
-        KDA_NORM_ROWS(1);
-    } else {
-        if (r.nv == 1) KDA_NORM_ROWS(1);
-        else if (r.nv == 2) KDA_NORM_ROWS(2);
-        else KDA_NORM_ROWS(4);
-    }
+    constexpr int kMost = LANES < 32 ? 1 : most_vectors(V, LANES);
+    if (r.nv == 1) KDA_NORM_ROWS(1);
+    if constexpr (kMost >= 2)
+        if (r.nv == 2) KDA_NORM_ROWS(2);
+    if constexpr (kMost >= 4)
+        if (r.nv == 4) KDA_NORM_ROWS(4);
+    if constexpr (kMost >= 8)
+        if (r.nv == 8) KDA_NORM_ROWS(8);
+    if constexpr (kMost >= 16)
+        if (r.nv == 16) KDA_NORM_ROWS(16);
 #undef KDA_NORM_ROWS
 #undef KDA_NORM_ROWS_OF
-    return cudaGetLastError();
+    return cudaErrorInvalidConfiguration;
 }
 
 template <typename T, int V, bool kBwd>

@@ -247,6 +247,14 @@ def test_group_norm(dtype, C, groups, silu, affine, lengths, per_token):
         assert dw is None and db is None
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("C,groups", [(435, 3), (501, 1), (690, 3), (514, 1), (1026, 2), (1025, 1), (2047, 1), (2050, 1), (4095, 1),
+                                      (4097, 1), (8190, 1), (8188, 1), (8193, 1), (16400, 1), (8200, 1)])
+def test_group_norm_rows_of_every_width(dtype, C, groups):
+    """Rows that a warp, a block or neither holds, in vectors of each width."""
+    test_group_norm(dtype, C, groups, True, True, [0, 3, 0, 200, 1, 64, 0], True)
+
+
 def test_group_norm_far_mean():
     """A mean of 4096 standard deviations costs no more than x's own step."""
     g, T, C = Gen(3), 500, 64
