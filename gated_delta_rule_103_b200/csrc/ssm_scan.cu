@@ -64,6 +64,9 @@ kda_ssm_scan_kernel(Params<T> p)
     // this lane's states of its pair's channels (a channel behind the last stands
     // for the last and is not stored)
     const int pair = lane / L, s0 = (lane % L) * 4;
+    // A sequence of several units takes every entry state from `ends`, its
+    // initial state too: the block of its last unit may write `fin` over it.
+    const bool chained = p.ends && !(seg == 0 && last);
     float A[2][4], h[2][4];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -75,7 +78,7 @@ kda_ssm_scan_kernel(Params<T> p)
             A[r][i] = ok ? p.A[row + i] * kLog2e : 0.f;
             h[r][i] = 0.f;
             if (ok && mode != kCarry) {
-                if (p.ends && seg > 0) h[r][i] = p.ends[(size_t)slot * p.D * p.S + row + i];
+                if (chained) h[r][i] = p.ends[(size_t)slot * p.D * p.S + row + i];
                 else if (p.init) h[r][i] = p.init[(size_t)n * p.D * p.S + row + i];
             }
         }
@@ -235,6 +238,7 @@ kda_ssm_scan_kernel(Params<T> p)
     }
 
     if (mode == kCarry || (mode == kOut && last && p.fin)) {
+        __syncwarp();  // every lane has its initial state, which `fin` may be
         float* to = mode == kCarry ? p.ends + (size_t)slot * p.D * p.S : p.fin + (size_t)n * p.D * p.S;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
