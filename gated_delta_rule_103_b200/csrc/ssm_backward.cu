@@ -117,7 +117,7 @@ kda_ssm_bwd_carry_kernel(BwdParams<T> p)
         const int c = pair * 2 + r < at.nch ? pair * 2 + r : at.nch - 1;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            A[r][i] = s0 + i < p.f.S ? p.f.A[(size_t)(at.c0 + c) * p.f.S + s0 + i] * kLog2e : 0.f;
+            A[r][i] = s0 + i < p.f.S ? rate(p.f.A[(size_t)(at.c0 + c) * p.f.S + s0 + i]) : 0.f;
             h[r][i] = R[r][i] = 0.f;
             P[r][i] = 1.f;
         }
@@ -217,7 +217,7 @@ kda_ssm_bwd_chain_kernel(const float* __restrict__ A, const float* __restrict__ 
     const int first = units.first(n);
     const size_t i0 = (size_t)((blockIdx.x - half) % per) * span, i1 = i0 + span < DS ? i0 + span : DS;
     for (size_t i = i0 + threadIdx.x; i < i1; i += 256) {
-        const float a = A[i] * kLog2e;
+        const float a = rate(A[i]);
         float c = d_fin ? d_fin[(size_t)n * DS + i] : 0.f;
         float* e = exits + (size_t)first * DS + i;
         const float* st = steps + (size_t)first * D + (unsigned)i / (unsigned)S;
@@ -295,7 +295,7 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const bool ok = s0 + i < S;
-            A[r][i] = ok ? p.f.A[row[r] + i] * kLog2e : 0.f;
+            A[r][i] = ok ? rate(p.f.A[row[r] + i]) : 0.f;
             c[r][i] = dA[r][i] = 0.f;
             if (ok) {
                 if (p.f.ends && !at.last) c[r][i] = p.exits[(size_t)at.slot * DS + row[r] + i];

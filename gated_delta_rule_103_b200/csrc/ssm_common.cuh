@@ -7,6 +7,8 @@
 // States are padded to 4 L with A = B = C = 0 behind S.
 #pragma once
 
+#include <cfloat>
+
 #include "layer.h"
 #include "layer_common.cuh"
 
@@ -62,6 +64,15 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
     return d;
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// A log2 e, held finite: a state with A = -inf (an -exp(A_log) that overflowed)
+// forgets at every step, but not at the steps of nothing behind a sequence's end
+// (dt = 0), where 0 * -inf would be NaN.
+__device__ __forceinline__ float rate(float A)
+{
+    const float a = A * kLog2e;
+    return a < -FLT_MAX ? -FLT_MAX : a;
+}
 
 // The decay e^(dt A) of one token from A log2 e.  A state carries the mean error
 // of its decays times the tokens it remembers.  The fast 2^x is a little low,
@@ -308,7 +319,7 @@ __device__ __forceinline__ void chain_states(int block, const float* __restrict_
     const int first = units.first(n);
     const size_t i0 = (size_t)(block % per) * span, i1 = i0 + span < DS ? i0 + span : DS;
     for (size_t i = i0 + threadIdx.x; i < i1; i += 256) {
-        const float a = A[i] * kLog2e;
+        const float a = rate(A[i]);
         float h = init ? init[(size_t)n * DS + i] : 0.f;
         float* e = ends + (size_t)first * DS + i;
         const float* st = steps + (size_t)first * D + (unsigned)i / (unsigned)S;

@@ -75,7 +75,7 @@ kda_ssm_scan_kernel(Params<T> p)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const bool ok = s0 + i < p.S;
-            A[r][i] = ok ? p.A[row + i] * kLog2e : 0.f;
+            A[r][i] = ok ? rate(p.A[row + i]) : 0.f;
             h[r][i] = 0.f;
             if (ok && mode != kCarry) {
                 if (chained) h[r][i] = p.ends[(size_t)slot * p.D * p.S + row + i];
@@ -326,7 +326,7 @@ kda_ssm_step_kernel(const T* __restrict__ u, const T* __restrict__ delta, const 
     row4(A + (size_t)d * S + s0, a);
     const float bias = delta_bias ? delta_bias[d] : 0.f, sk = skip ? skip[d] : 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] *= kLog2e;
+    for (int i = 0; i < 4; ++i) a[i] = rate(a[i]);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int n = n0 + r;

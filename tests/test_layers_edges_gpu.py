@@ -40,3 +40,39 @@ def test_ssm_scan_state_in_place(dtype, lengths, packed, D, S, cut):
         o, f = kda.ssm_scan_fwd(*args, **opt, initial_state=st, final_state=st, cu_seqlens=cu, softplus=True)
         assert f.data_ptr() == st.data_ptr()
         assert torch.equal(o, out) and torch.equal(st, fin)
+
+
+# ---- values at the ends of their range ---------------------------------------------
+
+@pytest.mark.parametrize("lengths,cut", [([17, 0, 40, 1], False), ([700, 129], True)])
+@pytest.mark.parametrize("S", [13, 16])
+def test_ssm_scan_state_that_forgets_at_once(lengths, cut, S):
+    """A = -inf (an -exp(A_log) that overflowed): the state is what the last
+    token put there.  Steps are above 0.01, so that A = -1e6 has the same decay,
+    zero, in 64 bits, and finite terms in the gradients' formulas."""
+    D, N, T = 24, len(lengths), sum(lengths)
+    g, bounds = base.Gen(72), ref.bounds_of(lengths)
+    assert not cut or kda.ssm_scan_fwd_workspace_bytes(1, T, D, S, 1, N, True, F32) > 0
+    args, opt = base.scan_inputs(g, (1, T), D, S, 1, F32)
+    args, cu = list(args), base.cu_of(lengths)
+    at_once = g.uniform(0.0, 1.0, D, S) < 0.3
+    s0, d_out, d_fin = g.normal(N, D, S), g.normal(1, T, D), g.normal(N, D, S)
+    leaves = [base.wide(t[0] if i != 2 else torch.where(at_once, -1e6, t)) for i, t in enumerate(args)]
+    leaves += [base.wide(opt["D"]), base.wide(opt["z"][0]), base.wide(opt["delta_bias"]), base.wide(s0)]
+    assert float(torch.nn.functional.softplus(leaves[1] + leaves[7]).detach().min()) > 0.01
+    o_ref, f_ref = ref.ssm_scan(*leaves[:8], leaves[8], bounds, True)
+    want = ref.grads_of((o_ref, f_ref), (d_out[0].cpu().double(), d_fin.cpu().double()), leaves)
+    for A in (float("-inf"), -3e38):
+        args[2] = torch.where(at_once, A, args[2])
+        out, fin = kda.ssm_scan_fwd(*args, **opt, initial_state=s0, cu_seqlens=cu, softplus=True)
+        base.near(out[0], o_ref, base.SCAN_TOL)
+        base.near(fin, f_ref, base.SCAN_TOL)
+        got = kda.ssm_scan_bwd(*args, d_out, **opt, initial_state=s0, d_final_state=d_fin, cu_seqlens=cu, softplus=True)
+        for v, r in zip(got, want):
+            base.near(v.reshape(r.shape), r, base.SCAN_TOL)
+        st = s0.clone()
+        for t in range(lengths[0]) if not cut else ():
+            one = [v[:, t].clone() if i != 2 else v for i, v in enumerate(args)]   # aligned, as a slice is not
+            y = kda.ssm_step(*one, st[:1], D=opt["D"], z=opt["z"][:, t].clone(),
+                             delta_bias=opt["delta_bias"], softplus=True)
+            base.near(y[0], o_ref[t], 4 * base.SCAN_TOL)
