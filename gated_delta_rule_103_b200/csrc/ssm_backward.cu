@@ -160,6 +160,8 @@ kda_ssm_bwd_carry_kernel(BwdParams<T> p)
             bc.load(p.f, t + TT, at.end, at.g, lane);
         }
         __syncwarp();
+        const float4 d0 = *reinterpret_cast<const float4*>(&s_dt[0][pair][0]);
+        const float mean[2] = {mean_error(d0.x, slowest(A[0])), mean_error(d0.z, slowest(A[1]))};
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt) {
             const float4 dd = *reinterpret_cast<const float4*>(&s_dt[tt][pair][0]);
@@ -171,7 +173,7 @@ kda_ssm_bwd_carry_kernel(BwdParams<T> p)
             for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float a = decay(r ? dd.z : dd.x, A[r][i]);
+                    const float a = decay(r ? dd.z : dd.x, A[r][i], mean[r]);
                     h[r][i] = fmaf(a, h[r][i], (r ? dd.w : dd.y) * B[i]);
                     P[r][i] *= a;
                     R[r][i] = fmaf(P[r][i], (r ? dy.y : dy.x) * C[i], R[r][i]);
@@ -321,7 +323,7 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
 
     Elements<T, Sh> el;
     StateRows<T, Sh, true> bc;
-    float h[2][4];
+    float h[2][4], mean[2];
     auto fetch = [&](int k) {
         const int t = at.t0 + k * TT;
         el.fetch(p, t + tok, at.end, own);
@@ -345,7 +347,7 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
         for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                h[r][i] = fmaf(decay(r ? dd.z : dd.x, A[r][i]), h[r][i], (r ? dd.w : dd.y) * B[i]);
+                h[r][i] = fmaf(decay(r ? dd.z : dd.x, A[r][i], mean[r]), h[r][i], (r ? dd.w : dd.y) * B[i]);
     };
 
     if (tiles > 0) fetch(tiles - 1);
@@ -376,6 +378,8 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
             }
         bc.put(s_B, s_C, tid);
         __syncthreads();
+        mean[0] = mean_error(s_dt[pair].x, slowest(A[0]));
+        mean[1] = mean_error(s_dt[pair].z, slowest(A[1]));
         // the states in front of every four tokens
 #pragma unroll
         for (int q = 0; q < TT / 4; ++q) {
@@ -406,7 +410,7 @@ kda_ssm_bwd_kernel(BwdParams<T> p)
                 for (int r = 0; r < 2; ++r)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        as[j][r][i] = decay(r ? dd.z : dd.x, A[r][i]);
+                        as[j][r][i] = decay(r ? dd.z : dd.x, A[r][i], mean[r]);
                         hs[j][r][i] = fmaf(as[j][r][i], j ? hs[j > 0 ? j - 1 : 0][r][i] : b[r][i], (r ? dd.w : dd.y) * B[i]);
                     }
             }

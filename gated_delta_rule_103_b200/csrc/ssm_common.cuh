@@ -75,12 +75,25 @@ __device__ __forceinline__ float rate(float A)
 }
 
 // The decay e^(dt A) of one token from A log2 e.  A state carries the mean error
-// of its decays times the tokens it remembers.  The fast 2^x is a little low,
-// measured over [-0.5, -0.001], where the long memories lie, by 1.7e-8 to 2e-8
-// of its value; the constant, that much in the exponent, takes it back (no
-// instruction: the product becomes a fused one).
-constexpr float kDecayMean = 1.8e-8f * kLog2e;
-__device__ __forceinline__ float decay(float dt, float A) { return ex2(fmaf(dt, A, kDecayMean)); }
+// of its decays times the tokens it remembers, 1 / |x| with x = dt A.  The fast
+// 2^x is low in the mean by 5e-9 to 7e-9 of its value for x within 2^-9 of zero,
+// by 1.2e-8 to 2.9e-8 from there to -1 (per octave of x, a million values each);
+// a constant in the exponent takes the middle of that back, at no instruction:
+// the product becomes a fused one.  Final states that remember 64, 256, 1024 and
+// 4096 tokens are off by 3e-7, 1.0e-6, 0.9e-6 and 2.3e-6 (without a constant by
+// 1.2e-6, 4.4e-6, 4.2e-6 and 1.5e-5; with 1.8e-8 for every x by 4e-7, 1.5e-6,
+// 8.6e-6 and 3.5e-5).  Which of the two applies is settled for a tile and four
+// states at a time, by the tile's first token and the slowest state (0 where
+// states are padding): 1 to 2 % of the scan's time, where one choice a decay
+// would add half as many instructions as the recurrence has.
+constexpr float kMeanLong = 6e-9f * kLog2e, kMean = 2.2e-8f * kLog2e;
+constexpr float kLongRate = -0.0027f * kLog2e;  // 2^-8.5
+__device__ __forceinline__ float slowest(const float (&A)[4])
+{
+    return fmaxf(fmaxf(A[0], A[1]), fmaxf(A[2], A[3]));
+}
+__device__ __forceinline__ float mean_error(float dt, float slow) { return dt * slow > kLongRate ? kMeanLong : kMean; }
+__device__ __forceinline__ float decay(float dt, float A, float mean) { return ex2(fmaf(dt, A, mean)); }
 
 // log(1 + e^x) = max(x, 0) + log1p(w), w = e^-|x|.  log1p(w) = 2 artanh(r)
 // with r = w / (2 + w) <= 1/3, by its power series to r^15 (the rest is below

@@ -186,7 +186,7 @@ kda_ssm_scan_kernel(Params<T> p)
         // Two tokens ahead: what is read from shared memory; one ahead: the
         // decays, so that neither's latency stands in the recurrence's way.
         float4 dd[3], B[3], C[3];
-        float a[2][2][4];
+        float a[2][2][4], mean[2];
         auto read = [&](int tt) {
             dd[tt % 3] = *reinterpret_cast<const float4*>(&s_dt[tt][pair][0]);
             B[tt % 3] = *reinterpret_cast<const float4*>(&s_B[tt * SP + s0]);
@@ -196,10 +196,12 @@ kda_ssm_scan_kernel(Params<T> p)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a[tt % 2][r][i] = decay(r ? dd[tt % 3].z : dd[tt % 3].x, A[r][i]);
+                for (int i = 0; i < 4; ++i) a[tt % 2][r][i] = decay(r ? dd[tt % 3].z : dd[tt % 3].x, A[r][i], mean[r]);
         };
         read(0);
         read(1);
+        mean[0] = mean_error(dd[0].x, slowest(A[0]));
+        mean[1] = mean_error(dd[0].z, slowest(A[1]));
         decays(0);
         size_t at = (size_t)(t + tok) * p.D;
 #pragma unroll
@@ -327,6 +329,7 @@ kda_ssm_step_kernel(const T* __restrict__ u, const T* __restrict__ delta, const 
     const float bias = delta_bias ? delta_bias[d] : 0.f, sk = skip ? skip[d] : 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] = rate(a[i]);
+    const float slow = slowest(a);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int n = n0 + r;
@@ -338,11 +341,11 @@ kda_ssm_step_kernel(const T* __restrict__ u, const T* __restrict__ delta, const 
         load_vec<1>(&dv[r], dd);
         float dt = dd[0] + bias;
         if (use_softplus) dt = softplus(dt);
-        const float du = dt * xx[0];
+        const float du = dt * xx[0], mean = mean_error(dt, slow);
         float hh[4] = {h[r].x, h[r].y, h[r].z, h[r].w}, y = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            hh[i] = fmaf(decay(dt, a[i]), hh[i], du * B[i]);
+            hh[i] = fmaf(decay(dt, a[i], mean), hh[i], du * B[i]);
             y = fmaf(hh[i], C[i], y);
         }
         const bool here = live && n < N;

@@ -76,3 +76,44 @@ def test_ssm_scan_state_that_forgets_at_once(lengths, cut, S):
             y = kda.ssm_step(*one, st[:1], D=opt["D"], z=opt["z"][:, t].clone(),
                              delta_bias=opt["delta_bias"], softplus=True)
             base.near(y[0], o_ref[t], 4 * base.SCAN_TOL)
+
+
+# ---- long memories -----------------------------------------------------------------
+
+@pytest.mark.parametrize("log_memory", [6, 7, 8, 10, 11, 12])
+def test_ssm_scan_long_memory(log_memory):
+    """Sequences that are not cut, of states that remember M tokens and terms of
+    one sign, so that the decays' errors do not cancel.
+
+    A decay is off by up to 2^-24 of its value in the mean square (a step just
+    below one is 2^-24, and the fast 2^x is good to about that) and its mean by
+    what the exponent's constant leaves: at most 1e-9 where M is above 2^9, 1e-8
+    below.  A state of M tokens carries sqrt(M / 2) times the one and M times
+    the other."""
+    M, D, S = 1 << log_memory, 2048, 128
+    T, g = 3 * M, base.Gen(81)
+    assert kda.ssm_scan_fwd_workspace_bytes(1, T, D, S, 1, 1, False, F32) == 0
+    dt = g.uniform(0.75, 1.25, 1, T, D) * (1.4 / M)
+    A, u, B = -g.uniform(1.0, 2.0, D, S) / 1.4, 1 / dt, torch.ones(1, T, 1, S, device="cuda")
+    _, fin = kda.ssm_scan_fwd(u, dt, A, B, B)
+    A64, h = A.double(), torch.zeros(D, S, dtype=torch.float64, device="cuda")
+    step, du = dt[0].double(), (dt[0].double() * u[0].double())
+    for t in range(T):
+        h = torch.exp(step[t][:, None] * A64).mul_(h).add_(du[t][:, None])
+    e = float(((fin[0] - h) / h).square().mean().sqrt())
+    tol = 2.0 ** -24 * (M / 2) ** 0.5 + M * (1e-9 if log_memory > 9 else 1e-8)
+    assert e <= tol, f"{e:.2e} > {tol:.2e}"
+
+
+def test_ssm_step_of_nothing_keeps_the_state():
+    """dt = 0: a decay of one, bit for bit, for every rate."""
+    g, N, D, S = base.Gen(82), 8, 512, 16
+    A, st, zero = -torch.exp(g.normal(D, S, std=4.0)), g.normal(N, D, S), torch.zeros(N, D, device="cuda")
+    A[:, :4] = torch.tensor([0.0, 1.0, float("-inf"), -3e38], device="cuda")
+    want, B = st.clone(), g.normal(N, 1, S)
+    kda.ssm_step(g.normal(N, D), zero, A, B, B, st)
+    assert torch.equal(st, want)
+    many = torch.zeros(N, 50, D, device="cuda")
+    _, fin = kda.ssm_scan_fwd(many, many, A, B.expand(N, 50, S)[:, :, None].contiguous(),
+                              B.expand(N, 50, S)[:, :, None].contiguous(), initial_state=st)
+    assert torch.equal(fin, want)
