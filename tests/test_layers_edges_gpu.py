@@ -117,3 +117,51 @@ def test_ssm_step_of_nothing_keeps_the_state():
     _, fin = kda.ssm_scan_fwd(many, many, A, B.expand(N, 50, S)[:, :, None].contiguous(),
                               B.expand(N, 50, S)[:, :, None].contiguous(), initial_state=st)
     assert torch.equal(fin, want)
+
+
+# ---- the activations' functions -----------------------------------------------------
+
+STEP = 2.0 ** -24      # half a step of fp32, relative
+
+
+def exp_error(x):
+    """e^x is good to 2^-22 (the fast 2^x) and |x| times the rounding of x log2 e
+    (2^-24) and of the constant (0.22 2^-24): in half steps."""
+    return 4 + 1.25 * x.abs()
+
+
+def test_fp32_silu_and_its_slope():
+    """Value by value over the whole range of e^x, through the convolution with
+    weights 0 and 1.  silu = v / (1 + e^-v): what e^-v is off by, a sum (1), a
+    reciprocal (2) and a product (1).  slope = s (1 + v (1 - s)): s (3 and e^-v's),
+    1 - s as far off as s and rounded, times v s, and three roundings."""
+    x = torch.linspace(-80, 80, 1 << 20, device="cuda").reshape(1, -1, 4).contiguous()
+    w = torch.tensor([0.0, 1.0], device="cuda").expand(4, 2).contiguous()
+    out, _ = kda.short_conv_fwd(x, w, activation="silu")
+    v = x.double()
+    s = torch.sigmoid(v)
+    off = exp_error(v) * (1 - s)                       # of e^-v / (1 + e^-v)
+    assert float(((out - v * s) / (v * s)).abs().div(off + 4).max()) <= STEP
+    dx = kda.short_conv_bwd(x, w, torch.ones_like(x), activation="silu")[0]
+    slope = s * (1 + v * (1 - s))
+    assert float(((dx - slope).abs() / ((off + 6) * slope.abs() + ((off + 3) * s + 1) * v.abs() * s)).max()) <= STEP
+    b = x[0, 5].clone()
+    normed = kda.group_norm_fwd(x, 4, torch.zeros(4, device="cuda"), b, activation="silu", per_token=True)[0]
+    want = (b.double() * torch.sigmoid(b.double())).expand_as(normed)
+    assert float(((normed - want) / want).abs().max()) <= float(exp_error(b).max() + 4) * STEP
+
+
+def test_fp32_softplus_keeps_its_precision_far_below_zero():
+    """The step alone, as the state that a token leaves in an empty one (u = B =
+    1).  What e^-|x| is off by, a sum (1), a reciprocal (2), four roundings around
+    the series, 3e-9 that it leaves out."""
+    D = 1 << 16
+    x = torch.linspace(-80, 20, D, device="cuda").reshape(1, D)
+    one, st = torch.ones_like(x), torch.zeros(1, D, 1, device="cuda")
+    A, B = -torch.ones(D, 1, device="cuda"), torch.ones(1, 1, 1, device="cuda")
+    kda.ssm_step(one, x, A, B, B, st, softplus=True)
+    want, tol = torch.logaddexp(x.double(), torch.zeros_like(x.double())), (exp_error(x) + 8) * STEP
+    assert float(((st[..., 0] - want).abs() / want / tol).max()) <= 1
+    # and in a scan, whose series runs on two values at a time
+    fin = kda.ssm_scan_fwd(one[None], x[None], A, B[None], B[None], softplus=True)[1]
+    assert float(((fin[..., 0] - want).abs() / want / tol).max()) <= 1
