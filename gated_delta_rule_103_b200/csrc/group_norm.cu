@@ -22,7 +22,9 @@
 // Sums of squares run over deviations: within a thread from the thread's first
 // value, across threads and units from the common mean,
 //     q = sum_i (q_i + n_i (m_i - m)^2),
-// so that a mean far from zero costs no digits.
+// so that a mean far from zero costs no digits.  Sums over many tokens run in
+// short chains, and their parts are added up in 64 bits: fp32 results are 0.8 to
+// 1.3e-7 from 64 bits, dweight and dbias of 27000 tokens too (2.1e-7 in one chain).
 #include "layer.h"
 #include "layer_common.cuh"
 
@@ -82,6 +84,13 @@ constexpr int rows_at_once(int values, bool bwd)
 {
     return values <= 2 || (values <= 4 && !bwd) ? 4 : values <= 8 ? 2 : 1;
 }
+// fp32: rows that a lane's sums for dweight and dbias run over before they go to
+// sums of those sums, in shared memory (chains of 8 and rows / 8 roundings; up to
+// 2 % of the time).  Not for bf16, whose inputs carry 2^-9: there the registers of
+// a lane with 32 values spill (16384 x 1024 in one group: 92 us against 68).
+constexpr int kRowsASum = 8;
+template <typename T>
+constexpr bool kSumsOfSums = sizeof(T) == 4;
 // Vectors of a row that a lane holds at most: 16 values in a warp's lane (32 in
 // vectors of 8), then the row takes the block; 32 in a block's, 16 in vectors of
 // one.  Forward and backward, SiLU, bf16: 3191 x 4640 in 32 groups (of 145: 5
@@ -117,6 +126,24 @@ kda_norm_rows_kernel(const T* __restrict__ x, const float* __restrict__ weight, 
     const float inv = 1.f / (float)Cg;
     constexpr int U = rows_at_once(V * NV, kBwd);
     __shared__ float red[LANES > 32 ? U : 1][8];
+    constexpr bool kSums = kBwd && kSumsOfSums<T>;
+    extern __shared__ float sums[];  // kSums: this thread's, [2][NV V][256]
+    float* own = sums + threadIdx.x;
+    if (kSums)
+#pragma unroll
+        for (int i = 0; i < 2 * NV * V; ++i) own[i * 256] = 0.f;
+    auto flush = [&] {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float& a = dw[kBwd ? i : 0][j];
+                float& c = db[kBwd ? i : 0][j];
+                own[(i * V + j) * 256] += a;
+                own[((NV + i) * V + j) * 256] += c;
+                a = c = 0.f;
+            }
+    };
     const int steps = (rows + walkers - 1) / walkers;
     for (int s = 0; s < steps; s += U) {
         size_t at[U];
@@ -234,14 +261,23 @@ kda_norm_rows_kernel(const T* __restrict__ x, const float* __restrict__ weight, 
                     store_vec<V>(grad_x + at[q] + i * LANES * V, dx);
                 }
             }
+            if (kSums && (s + U) % kRowsASum == 0) flush();
         }
     }
     if (kBwd && live) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (!in(i)) continue;
-            store_vec<V>(part + ((size_t)k * 2) * C + col + i * LANES * V, dw[kBwd ? i : 0]);
-            store_vec<V>(part + ((size_t)k * 2 + 1) * C + col + i * LANES * V, db[kBwd ? i : 0]);
+            float (&a)[V] = dw[kBwd ? i : 0];
+            float (&c)[V] = db[kBwd ? i : 0];
+            if (kSums)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    a[j] += own[(i * V + j) * 256];
+                    c[j] += own[((NV + i) * V + j) * 256];
+                }
+            store_vec<V>(part + ((size_t)k * 2) * C + col + i * LANES * V, a);
+            store_vec<V>(part + ((size_t)k * 2 + 1) * C + col + i * LANES * V, c);
         }
     }
 }
@@ -351,10 +387,14 @@ struct Layout {
     int len;                              // tokens per unit
 };
 
-// One unit's tokens of the column at p, ty apart, kBatch rows in flight.
+// One unit's tokens of the column at p, ty apart, kBatch rows in flight.  `f` is
+// told which is a batch's first, `done` follows its last: sums run over a batch
+// first, so that the chains of roundings are short.  (The backward pass's sums over
+// two tensors' rows run on: batches cost them 18 % and left dweight at 1.1e-7 of
+// 64 bits instead of 1.3e-7.)
 constexpr int kBatch = 8;
-template <typename T, int V, typename F>
-__device__ __forceinline__ void each_token(const T* p, int a, int b, int C, int ty, F&& f)
+template <typename T, int V, typename F, typename E>
+__device__ __forceinline__ void each_token(const T* p, int a, int b, int C, int ty, F&& f, E&& done)
 {
     for (int t = a; t < b; t += kBatch * ty) {
         Raw<T, V> r[kBatch];
@@ -366,8 +406,9 @@ __device__ __forceinline__ void each_token(const T* p, int a, int b, int C, int 
             if (t + i * ty < b) {
                 float v[V];
                 r[i].get(v);
-                f(t + i * ty, v);
+                f(t + i * ty, i == 0, v);
             }
+        done();
     }
 }
 // ... of the columns at p and q
@@ -415,16 +456,19 @@ kda_norm_stats_kernel(const T* __restrict__ x, float* __restrict__ part, Units u
         const float rows = (float)((b - a - ty + l.ty - 1) / l.ty * V);
         for (int c = cx; c < groups * l.cpg; c += wide ? l.threads : l.cols) {
             const T* p = x + ((size_t)g0 * l.cpg + c) * V;
-            float first[V], s1 = 0.f, s2 = 0.f;
+            float first[V], s1 = 0.f, s2 = 0.f, b1, b2;
             load_vec<V>(p + (size_t)(a + ty) * C, first);
             const float k = first[0];
-            each_token<T, V>(p, a + ty, b, C, l.ty, [&](int, const float (&v)[V]) {
+            each_token<T, V>(p, a + ty, b, C, l.ty, [&](int, bool start, const float (&v)[V]) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const float d = v[j] - k;
-                    s1 += d;
-                    s2 = fmaf(d, d, s2);
+                    b1 = start && j == 0 ? d : b1 + d;
+                    b2 = start && j == 0 ? d * d : fmaf(d, d, b2);
                 }
+            }, [&] {
+                s1 += b1;
+                s2 += b2;
             });
             const float d = s1 / rows, m = k + d, q = fmaxf(s2 - s1 * d, 0.f);
             // another column of the same group (wide): shares by the counts
@@ -466,53 +510,51 @@ kda_norm_stats_kernel(const T* __restrict__ x, float* __restrict__ part, Units u
 }
 
 // Sum over a block's rows of 32 lanes, for every lane; red is [32][33].
-__device__ __forceinline__ float rows_sum(float v, float (*red)[33])
+__device__ __forceinline__ double rows_sum(double v, double (*red)[33])
 {
     const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
     __syncthreads();
     red[y][lane] = v;
     __syncthreads();
-    float s = 0.f;
+    double s = 0.0;
 #pragma unroll
     for (int i = 0; i < 32; ++i) s += red[i][lane];
     return s;
 }
 
 // mean and rstd of every (sequence, group): a block takes 32 groups of a
-// sequence, its 32 warps the sequence's units in turn.
+// sequence, its 32 warps the sequence's units in turn.  In 64 bits: one number's
+// sum of 32 and more parts would lose what its threads' sums have kept.
 __global__ void __launch_bounds__(1024)
 kda_norm_merge_kernel(const float* __restrict__ part, float* __restrict__ mean, float* __restrict__ rstd,
                       Units units, int G, int Cg, int across, float eps)
 {
-    __shared__ float red[32][33];
+    __shared__ double red[32][33];
     const int n = blockIdx.x / across, lane = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int g = (int)(blockIdx.x % across) * 32 + lane, gg = g < G ? g : G - 1;
     int a, b;
     units.s.bounds(n, a, b);
     const int cnt = b > a ? units.count_of(a, b) : 0;
     const float2* p = reinterpret_cast<const float2*>(part) + (size_t)units.first(n) * G + gg;
-    const float inv = b > a ? 1.f / ((float)(b - a) * (float)Cg) : 0.f;
-    const float k = cnt ? p[0].x : 0.f;
+    const double inv = b > a ? 1.0 / ((double)(b - a) * Cg) : 0.0;
     auto weight = [&](int i) {  // values of unit i
         const int left = b - a - i * units.len;
-        return (float)(left < units.len ? left : units.len) * (float)Cg;
+        return (double)(left < units.len ? left : units.len) * Cg;
     };
-    float s1 = 0.f, s2 = 0.f, rest = 0.f;
+    double s1 = 0.0, s2 = 0.0;
 #pragma unroll 4
-    for (int i = y; i < cnt; i += 32) s1 = fmaf(weight(i), p[(size_t)i * G].x - k, s1);
-    float m = fmaf(rows_sum(s1, red), inv, k);
+    for (int i = y; i < cnt; i += 32) s1 = fma(weight(i), (double)p[(size_t)i * G].x, s1);
+    const double m = rows_sum(s1, red) * inv;
 #pragma unroll 4
     for (int i = y; i < cnt; i += 32) {
         const float2 v = p[(size_t)i * G];
-        const float e = v.x - m;
-        rest = fmaf(weight(i), e, rest);  // what k's rounding left of the mean
-        s2 += fmaf(weight(i) * e, e, v.y);
+        const double e = (double)v.x - m;
+        s2 += fma(weight(i) * e, e, (double)v.y);
     }
     s2 = rows_sum(s2, red);
-    m = fmaf(rows_sum(rest, red), inv, m);
     if (y == 0 && g < G) {
-        mean[(size_t)n * G + g] = m;  // 0 of an empty sequence
-        rstd[(size_t)n * G + g] = 1.f / sqrtf(fmaf(s2, inv, eps));
+        mean[(size_t)n * G + g] = (float)m;  // 0 of an empty sequence
+        rstd[(size_t)n * G + g] = (float)(1.0 / sqrt(fma(s2, inv, (double)eps)));
     }
 }
 
@@ -545,14 +587,14 @@ kda_norm_apply_kernel(const T* __restrict__ x, const float* __restrict__ weight,
             bb[j] = bias ? bias[ch + j] : 0.f;
         }
         if constexpr (!kBwd) {
-            each_token<T, V>(x + ch, a + ty, b, C, l.ty, [&](int t, float (&v)[V]) {
+            each_token<T, V>(x + ch, a + ty, b, C, l.ty, [&](int t, bool, float (&v)[V]) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     v[j] = fmaf((v[j] - m) * rs, w[j], bb[j]);
                     if (act) v[j] = silu(v[j]);
                 }
                 store_vec<V>(out + (size_t)t * C + ch, v);
-            });
+            }, [] {});
         } else {
             const float k1 = sums[ng * 2], k2 = sums[ng * 2 + 1];
             each_token2<T, V>(x + ch, d_out + ch, a + ty, b, C, l.ty, [&](int t, float (&v)[V], float (&dy)[V]) {
@@ -677,17 +719,17 @@ kda_norm_bwd_sums_kernel(const T* __restrict__ x, const float* __restrict__ weig
 
 // From the parts: the parameters' gradients (the first blocks; 32 channels
 // each, 32 warps over the parts), and of every (sequence, group) the means of
-// k and k xhat (the others; 32 groups of a sequence each).
+// k and k xhat (the others; 32 groups of a sequence each), in 64 bits.
 __global__ void __launch_bounds__(1024)
 kda_norm_bwd_merge_kernel(const float* __restrict__ part, float* __restrict__ grad_weight,
                           float* __restrict__ grad_bias, long long parts, const float* __restrict__ gsum,
                           float* __restrict__ sums, Units units, int C, int G, int param_blocks, int across)
 {
-    __shared__ float red[2][32][33];
+    __shared__ double red[2][32][33];
     const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
     if ((int)blockIdx.x < param_blocks) {
         const int c = blockIdx.x * 32 + lane;
-        float sw = 0.f, sb = 0.f;
+        double sw = 0.0, sb = 0.0;
         if (c < C)
 #pragma unroll 4
             for (long long i = y; i < parts; i += 32) {
@@ -698,11 +740,11 @@ kda_norm_bwd_merge_kernel(const float* __restrict__ part, float* __restrict__ gr
         red[1][y][lane] = sb;
         __syncthreads();
         if (y < 2 && c < C) {
-            float t = 0.f;
+            double t = 0.0;
 #pragma unroll
             for (int k = 0; k < 32; ++k) t += red[y][k][lane];
-            if (y == 0 && grad_weight) grad_weight[c] = t;
-            if (y == 1 && grad_bias) grad_bias[c] = t;
+            if (y == 0 && grad_weight) grad_weight[c] = (float)t;
+            if (y == 1 && grad_bias) grad_bias[c] = (float)t;
         }
         return;
     }
@@ -712,7 +754,7 @@ kda_norm_bwd_merge_kernel(const float* __restrict__ part, float* __restrict__ gr
     units.s.bounds(n, a, b);
     const int cnt = b > a ? units.count_of(a, b) : 0;
     const float2* p = reinterpret_cast<const float2*>(gsum) + (size_t)units.first(n) * G + gg;
-    float s1 = 0.f, s2 = 0.f;
+    double s1 = 0.0, s2 = 0.0;
 #pragma unroll 4
     for (int i = y; i < cnt; i += 32) {
         const float2 v = p[(size_t)i * G];
@@ -722,9 +764,9 @@ kda_norm_bwd_merge_kernel(const float* __restrict__ part, float* __restrict__ gr
     s1 = rows_sum(s1, red[0]);
     s2 = rows_sum(s2, red[0]);
     if (y == 0 && g < G) {
-        const float inv = cnt ? 1.f / ((float)(b - a) * (float)(C / G)) : 0.f;
-        sums[((size_t)n * G + g) * 2] = s1 * inv;
-        sums[((size_t)n * G + g) * 2 + 1] = s2 * inv;
+        const double inv = cnt ? 1.0 / ((double)(b - a) * (C / G)) : 0.0;
+        sums[((size_t)n * G + g) * 2] = (float)(s1 * inv);
+        sums[((size_t)n * G + g) * 2 + 1] = (float)(s2 * inv);
     }
 }
 
@@ -815,9 +857,16 @@ cudaError_t rows_nv(const NormArgs& a, const RowShape& r, cudaStream_t st)
     constexpr bool kWhole = LANES == 1 || V == 16 / (int)sizeof(T);
     const bool full = r.lanes * r.nv * V == a.C / a.G;
 #define KDA_NORM_ROWS_OF(NV, FULL)                                                                             \
-    kda_norm_rows_kernel<T, V, LANES, NV, FULL, kBwd><<<(unsigned)r.blocks, 256, 0, st>>>(                     \
-        (const T*)a.x, a.weight, a.bias, (T*)a.out, a.mean, a.rstd, (const T*)a.d_out, a.grad_x,               \
-        (float*)a.workspace, rows, a.G, a.C / a.G, r.walkers, a.eps, a.silu)
+    do {                                                                                                       \
+        auto* kernel = &kda_norm_rows_kernel<T, V, LANES, NV, FULL, kBwd>;                                     \
+        constexpr int smem = kBwd && kSumsOfSums<T> ? 2 * NV * V * 256 * (int)sizeof(float) : 0;               \
+        if constexpr (smem > 32 * 1024)                                                                        \
+            if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) \
+                return e;                                                                                      \
+        kernel<<<(unsigned)r.blocks, 256, smem, st>>>((const T*)a.x, a.weight, a.bias, (T*)a.out, a.mean,      \
+            a.rstd, (const T*)a.d_out, a.grad_x, (float*)a.workspace, rows, a.G, a.C / a.G, r.walkers, a.eps,  \
+            a.silu);                                                                                           \
+    } while (0)
 #define KDA_NORM_ROWS(NV)                                                                                      \
     do {                                                                                                       \
         if constexpr (kWhole) {                                                                                \

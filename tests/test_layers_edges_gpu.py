@@ -165,3 +165,41 @@ def test_fp32_softplus_keeps_its_precision_far_below_zero():
     # and in a scan, whose series runs on two values at a time
     fin = kda.ssm_scan_fwd(one[None], x[None], A, B[None], B[None], softplus=True)[1]
     assert float(((fin[..., 0] - want).abs() / want / tol).max()) <= 1
+
+
+# ---- sums over many tokens -----------------------------------------------------------
+
+# A rounding to fp32 is uniform within half a step, which is 2^-25 to 2^-24 of the
+# value: 0.42 2^-24 in the mean square.
+ROUNDING = 0.42 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("T,C,groups", [(26884, 784, 8), (16384, 1024, 32), (8192, 4096, 1), (32768, 258, 2)])
+def test_group_norm_parameter_sums_per_token(T, C, groups):
+    """dbias is the plain sum of d_out: chains of 8 rows, then of a walker's
+    rows / 8 (at most 32 where the kernels hold 444 and more), then 64 bits.  The
+    n-th partial sum of random terms is sqrt(n / N) of the whole, so a chain of N
+    costs sqrt(N / 2) roundings.  Twice that, for what is not in the mean."""
+    g = base.Gen(91)
+    x, d = g.normal(1, T, C), g.normal(1, T, C)
+    w, b = torch.ones(C, device="cuda"), torch.zeros(C, device="cuda")
+    _, mean, rstd = kda.group_norm_fwd(x, groups, w, b, per_token=True)
+    _, dw, db = kda.group_norm_bwd(x, groups, d, mean, rstd, w, b, per_token=True)
+    tol = 2 * ROUNDING * (8 / 2 + 8 / 2 + 1) ** 0.5
+    d64, x64 = d[0].double(), x[0].double().view(T, groups, -1)
+    assert base.rel_fro(db, d64.sum(0).cpu()) <= tol
+    # dweight: xhat's own two roundings beside the mean's and rstd's, up to 2^-24 each
+    xh = (x64 - x64.mean(-1, keepdim=True)) / (x64.var(-1, correction=0, keepdim=True) + 1e-5).sqrt()
+    assert base.rel_fro(dw, (xh.view(T, C) * d64).sum(0).cpu()) <= tol + 2 * 2.0 ** -24
+
+
+def test_group_norm_statistics_of_long_sequences():
+    """rstd is rounded once where its parts are added up in 64 bits; a sequence's
+    170 threads leave the mean of their sums' roundings (of squares: chains of 32
+    and 16 terms, sqrt(48 / 3) each, half of it in the root).  Half as much again."""
+    N, T, C, groups = 11, 2182, 640, 32
+    g = base.Gen(92)
+    x = g.normal(N, T, C) + g.normal(C)
+    _, _, rstd = kda.group_norm_fwd(x, groups)
+    want = (x.double().view(N, T, groups, -1).var((1, 3), correction=0) + 1e-5).rsqrt()
+    assert base.rel_fro(rstd, want.cpu()) <= 1.5 * ROUNDING * (1 + 4 / 2 / 170 ** 0.5)
