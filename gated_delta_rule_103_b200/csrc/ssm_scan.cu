@@ -309,7 +309,9 @@ kda_ssm_step_kernel(const T* __restrict__ u, const T* __restrict__ delta, const 
     for (int r = 0; r < R; ++r) {
         const int n = n0 + r < N ? n0 + r : N - 1;
         const float* st = state + ((size_t)n * D + d) * S + s0;
-        if (kVec && s0 < S) {
+        if (!live) {
+            h[r] = make_float4(0.f, 0.f, 0.f, 0.f);  // channel 0's is written meanwhile
+        } else if (kVec && s0 < S) {
             h[r] = __ldcs(reinterpret_cast<const float4*>(st));
         } else {
             float v[4];

@@ -203,3 +203,22 @@ def test_group_norm_statistics_of_long_sequences():
     _, _, rstd = kda.group_norm_fwd(x, groups)
     want = (x.double().view(N, T, groups, -1).var((1, 3), correction=0) + 1e-5).rsqrt()
     assert base.rel_fro(rstd, want.cpu()) <= 1.5 * ROUNDING * (1 + 4 / 2 / 170 ** 0.5)
+
+
+# ---- single tokens ------------------------------------------------------------------
+
+@pytest.mark.parametrize("N", [3, 5000])
+@pytest.mark.parametrize("D,S", [(65, 16), (7, 5), (300, 128), (257, 3)])
+def test_ssm_step_channels_that_do_not_fill_a_block(N, D, S):
+    """Threads behind the last channel: the states, channel 0's among them, and
+    the outputs are those of a scan over one token."""
+    if N * D * S > 1 << 25:
+        N = 300
+    g = base.Gen(95)
+    args, opt = base.scan_inputs(g, (N, 1), D, S, 1, F32)
+    st = g.normal(N, D, S)
+    out, fin = kda.ssm_scan_fwd(*args, **opt, initial_state=st, softplus=True)
+    one = [t[:, 0].contiguous() if i != 2 else t for i, t in enumerate(args)]
+    y = kda.ssm_step(*one, st, D=opt["D"], z=opt["z"][:, 0].contiguous(), delta_bias=opt["delta_bias"], softplus=True)
+    base.near(st, fin.double().cpu(), 8 * STEP)     # the same decays and terms, a product apart
+    base.near(y, out[:, 0].double().cpu(), S * STEP + 8 * STEP)
