@@ -3,6 +3,7 @@
 // fp32, the activations, and where the tokens of a packed batch belong.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -234,12 +235,14 @@ struct Units {
 // SMs of the current device.
 inline int sm_count()
 {
-    static int known[64] = {};  // a device's count does not change: any thread writes the same
+    static std::atomic<int> known[64];  // by device; a count does not change: any thread stores the same
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) != cudaSuccess) return sms;
-    if (dev >= 0 && dev < 64 && known[dev]) return known[dev];
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (dev >= 0 && dev < 64) known[dev] = sms;
+    const bool slot = dev >= 0 && dev < 64;
+    if (slot)
+        if (const int n = known[dev].load(std::memory_order_relaxed)) return n;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+    if (slot) known[dev].store(sms, std::memory_order_relaxed);
     return sms;
 }
 
