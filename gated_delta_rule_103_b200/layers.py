@@ -19,6 +19,7 @@ from .binding import (KDA_DTYPE_BF16, KDA_DTYPE_F32, KDA_FLAG_PER_TOKEN, KDA_FLA
                       KDA_FLAG_SOFTPLUS, KDAError, load_library)
 
 _F32, _BF16 = torch.float32, torch.bfloat16
+_INT_MAX = 2 ** 31 - 1
 _ACTIVATIONS = {None: 0, "silu": KDA_FLAG_SILU}
 
 
@@ -56,6 +57,7 @@ def _sequences(cu: Optional[torch.Tensor], B: int) -> Tuple[Optional[int], int]:
         raise TypeError("cu_seqlens must be a 1-D int32 tensor of N + 1 bounds")
     if B != 1:
         raise ValueError("packed sequences need a batch of 1")
+    _rank(cu, "cu_seqlens", 1)
     return _take(cu, "cu_seqlens", cu.shape, torch.int32), cu.numel() - 1
 
 
@@ -69,7 +71,19 @@ def _activation(name) -> int:
 def _rank(t: torch.Tensor, name: str, n: int):
     if t.dim() != n:
         raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
-    return t.shape
+    shape = t.shape
+    if max(shape) > _INT_MAX:      # ctypes would take it modulo 2^32
+        raise ValueError(f"{name} must have sizes below 2^31, got {tuple(shape)}")
+    return shape
+
+
+def _bytes(f, dtype, *sizes) -> int:
+    """A workspace query; 0, as for every size that a call refuses, where one is
+    no int of the library's."""
+    if not all(-1 < n <= _INT_MAX for n in sizes):
+        return 0
+    dt = KDA_DTYPE_BF16 if dtype == torch.bfloat16 else KDA_DTYPE_F32
+    return int(f(*sizes, dt))
 
 
 class _On:
@@ -198,8 +212,7 @@ def short_conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor,
 def short_conv_bwd_workspace_bytes(B: int, T: int, C: int, W: int, N: int, packed: bool,
                                    dtype=torch.bfloat16) -> int:
     """``kda_short_conv_bwd_workspace_bytes`` (``packed``: cu_seqlens is passed)."""
-    dt = KDA_DTYPE_BF16 if dtype == torch.bfloat16 else KDA_DTYPE_F32
-    return int(load_library().kda_short_conv_bwd_workspace_bytes(B, T, C, W, N, int(packed), dt))
+    return _bytes(load_library().kda_short_conv_bwd_workspace_bytes, dtype, B, T, C, W, N, int(packed))
 
 
 def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, d_out: torch.Tensor,
@@ -250,15 +263,13 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, d_out: torch.Tensor,
 def ssm_scan_fwd_workspace_bytes(B: int, T: int, D: int, S: int, G: int, N: int, packed: bool,
                                  dtype=torch.bfloat16) -> int:
     """``kda_ssm_scan_fwd_workspace_bytes`` (0: the call needs none)."""
-    dt = KDA_DTYPE_BF16 if dtype == torch.bfloat16 else KDA_DTYPE_F32
-    return int(load_library().kda_ssm_scan_fwd_workspace_bytes(B, T, D, S, G, N, int(packed), dt))
+    return _bytes(load_library().kda_ssm_scan_fwd_workspace_bytes, dtype, B, T, D, S, G, N, int(packed))
 
 
 def ssm_scan_bwd_workspace_bytes(B: int, T: int, D: int, S: int, G: int, N: int, packed: bool,
                                  dtype=torch.bfloat16) -> int:
     """``kda_ssm_scan_bwd_workspace_bytes``."""
-    dt = KDA_DTYPE_BF16 if dtype == torch.bfloat16 else KDA_DTYPE_F32
-    return int(load_library().kda_ssm_scan_bwd_workspace_bytes(B, T, D, S, G, N, int(packed), dt))
+    return _bytes(load_library().kda_ssm_scan_bwd_workspace_bytes, dtype, B, T, D, S, G, N, int(packed))
 
 
 def _scan_inputs(u, delta, A, B, C, D, z, delta_bias, lead: int):
@@ -388,8 +399,8 @@ def group_norm_workspace_bytes(B: int, T: int, C: int, groups: int, N: int, pack
     """``kda_group_norm_fwd_workspace_bytes`` (or ``_bwd_`` when ``backward``)."""
     lib = load_library()
     f = lib.kda_group_norm_bwd_workspace_bytes if backward else lib.kda_group_norm_fwd_workspace_bytes
-    dt = KDA_DTYPE_BF16 if dtype == torch.bfloat16 else KDA_DTYPE_F32
-    return int(f(B, T, C, groups, N, int(packed), dt, KDA_FLAG_PER_TOKEN if per_token else 0))
+    flags = KDA_FLAG_PER_TOKEN if per_token else 0
+    return _bytes(lambda *a: f(*a, flags), dtype, B, T, C, groups, N, int(packed))
 
 
 def _norm_inputs(x, groups, weight, bias, activation, per_token, cu_seqlens):
