@@ -396,25 +396,26 @@ kda_short_conv_bwd_kernel(const T* __restrict__ x, const float* __restrict__ wei
 }
 
 // grad_weight[c, j] and grad_bias[c] from the tiles' parts: 32 channels of one
-// tap per block, eight tile lanes.
+// tap per block, eight tile lanes.  In 64 bits: of 131072 tokens, 256 parts in
+// fp32 left dweight 2.5e-7 from 64 bits.
 __global__ void __launch_bounds__(256)
 kda_short_conv_params_kernel(const float* __restrict__ part, float* __restrict__ grad_weight,
                              float* __restrict__ grad_bias, int C, int W, int tiles)
 {
-    __shared__ float red[8][33];
+    __shared__ double red[8][33];
     const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane, j = blockIdx.y;
-    float s = 0.f;
+    double s = 0.0;
     if (c < C)
         for (int i = y; i < tiles; i += 8) s += part[((size_t)i * (W + 1) + j) * C + c];
     red[y][lane] = s;
     __syncthreads();
     if (y == 0 && c < C) {
-        float t = 0.f;
+        double t = 0.0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) t += red[k][lane];
-        if (j < W) grad_weight[(size_t)c * W + j] = t;
-        else if (grad_bias) grad_bias[c] = t;
+        if (j < W) grad_weight[(size_t)c * W + j] = (float)t;
+        else if (grad_bias) grad_bias[c] = (float)t;
     }
 }
 

@@ -222,3 +222,23 @@ def test_ssm_step_channels_that_do_not_fill_a_block(N, D, S):
     y = kda.ssm_step(*one, st, D=opt["D"], z=opt["z"][:, 0].contiguous(), delta_bias=opt["delta_bias"], softplus=True)
     base.near(st, fin.double().cpu(), 8 * STEP)     # the same decays and terms, a product apart
     base.near(y, out[:, 0].double().cpu(), S * STEP + 8 * STEP)
+
+
+@pytest.mark.parametrize("T,C", [(131072, 64), (65536, 33)])
+def test_short_conv_parameter_sums(T, C):
+    """dbias is the plain sum of d_out: a thread's run of up to 32 tokens, then a
+    block's up to 256 runs, then 64 bits; dweight has a rounded product fused into
+    the first.  A chain of N costs sqrt(N / 2) roundings, a chain over runs none
+    that the run's own share does not shrink: half as much again in all."""
+    g = base.Gen(96)
+    x, d, w = g.normal(1, T, C), g.normal(1, T, C), g.normal(C, 4)
+    _, dw, db, _ = kda.short_conv_bwd(x, w, d, bias=torch.zeros(C, device="cuda"), need_initial_state_grad=False)
+    d64 = d[0].double()
+    tx = 1
+    while tx < min(32, -(-C // (4 if C % 4 == 0 else 1))):
+        tx *= 2
+    tol = 1.5 * ROUNDING * (32 / 2 + 256 // tx / 2 + 1) ** 0.5
+    assert base.rel_fro(db, d64.sum(0).cpu()) <= tol
+    ext = torch.nn.functional.pad(x[0].double(), (0, 0, 3, 0))
+    want = torch.stack([(ext[j:j + T] * d64).sum(0) for j in range(4)], 1)
+    assert base.rel_fro(dw, want.cpu()) <= tol
