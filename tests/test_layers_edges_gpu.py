@@ -242,3 +242,40 @@ def test_short_conv_parameter_sums(T, C):
     ext = torch.nn.functional.pad(x[0].double(), (0, 0, 3, 0))
     want = torch.stack([(ext[j:j + T] * d64).sum(0) for j in range(4)], 1)
     assert base.rel_fro(dw, want.cpu()) <= tol
+
+
+# ---- paths of the scan that no usual case takes ---------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("state", [True, False])
+@pytest.mark.parametrize("T,D,S,G", [(333, 40, 16, 2), (449, 21, 3, 1), (150, 130, 100, 1)])
+def test_ssm_scan_cut_batch(dtype, state, T, D, S, G):
+    """A batch of equal sequences, cut: each row's units, entry states and final
+    state are its own."""
+    N = 3
+    assert kda.ssm_scan_fwd_workspace_bytes(N, T, D, S, G, N, False, dtype) > 0
+    g = base.Gen(97)
+    args, opt = base.scan_inputs(g, (N, T), D, S, G, dtype)
+    base.check_scan((N, T), [T * i for i in range(N + 1)], None, args, opt, g.normal(N, D, S) if state else None,
+                    g.normal(N, T, D, dtype=dtype), g.normal(N, D, S) if state else None)
+
+
+@pytest.mark.parametrize("S", [3, 16, 100])
+def test_ssm_scan_steps_of_nothing_behind_a_token(S):
+    """A token of any size, then dt = 0: the state and what is read from it stay,
+    bit for bit, through the rest of its tile and the next ones; so do adjoints
+    on their way back."""
+    g, T, D = base.Gen(98), 37, 64
+    A, B, C = -g.uniform(0.001, 4.0, D, S), g.normal(1, T, 1, S), g.normal(1, 1, 1, S).expand(1, T, 1, S).contiguous()
+    u, dt, s0 = g.normal(1, T, D), torch.zeros(1, T, D, device="cuda"), g.normal(1, D, S)
+    dt[:, 0] = g.uniform(0.001, 2.0, D)
+    out, fin = kda.ssm_scan_fwd(u, dt, A, B, C, initial_state=s0)
+    one, first = kda.ssm_scan_fwd(u[:, :1].clone(), dt[:, :1].clone(), A, B[:, :1].clone(), C[:, :1].clone(),
+                                  initial_state=s0)
+    assert torch.equal(fin, first)
+    assert torch.equal(out, one.expand(1, T, D))
+    d_fin = g.normal(1, D, S)
+    ds = kda.ssm_scan_bwd(u, dt, A, B, C, torch.zeros_like(u), initial_state=s0, d_final_state=d_fin)[8]
+    ds1 = kda.ssm_scan_bwd(u[:, :1].clone(), dt[:, :1].clone(), A, B[:, :1].clone(), C[:, :1].clone(),
+                           torch.zeros(1, 1, D, device="cuda"), initial_state=s0, d_final_state=d_fin)[8]
+    assert torch.equal(ds, ds1)
