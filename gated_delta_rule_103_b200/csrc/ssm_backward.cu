@@ -580,9 +580,11 @@ kda_ssm_bwd_sums_kernel(const float* __restrict__ part_bc, float* __restrict__ g
 }
 
 // Sequences are cut where the chains give the SMs fewer warps than this: another
-// walk then goes over most tokens, a fifth of the whole.  (4 x 1024 x 4096, 6.9
-// warps an SM: 757 us whole, 916 us cut; units for 16 warps of at least 32 tokens
-// against 8 and 64: 17245 x 640 628 against 676 us, small calls 5 to 20 % less.)
+// walk then goes over most tokens, a fifth of the whole.  Forward and backward of
+// 4096 channels, 16 states, bf16, whole against cut: 1 x 4096 tokens (1.7 warps an
+// SM) 2133 and 881 us, 2 x 2048 (3.5) 1088 and 944, 3 x 1365 (5.2) 970 and 993, 4 x
+// 1024 (6.9) 734 and 1003.  Units for 16 warps of at least 32 tokens against 8 and
+// 64: 17245 x 640 628 against 676 us, small calls 5 to 20 % less.
 constexpr int kBwdFewWarps = 5, kBwdWantWarps = 16, kBwdShortest = 32;
 
 struct Layout {

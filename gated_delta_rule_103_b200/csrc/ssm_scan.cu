@@ -370,16 +370,23 @@ kda_ssm_step_kernel(const T* __restrict__ u, const T* __restrict__ delta, const 
     }
 }
 
-// A unit's tokens are passed over twice where sequences are cut, which pays where
-// the SMs have under six warps each (3.5 warps: 930 us whole, 533 us cut; 6.9
-// warps: 529 us whole, 1088 us cut), and then into units for sixteen warps each
-// (20011 tokens of 1100 channels: 283 us, 348 us for twelve).  The two launches
-// more are worth some hundred tokens.
-constexpr int kFewWarps = 6, kWantWarps = 16, kShortest = 32, kLeast = 128;
+// A unit's tokens are passed over twice where sequences are cut, and whole ones
+// take as long as their chain is, so what decides is how many warps the chains give
+// an SM.  bf16, 16 states, whole against cut: 1 x 16384 tokens of 4096 channels (1.7
+// warps) 1466 and 812 us, 7 x 2340 of 1024 (3.0) 217 and 258, 2 x 8192 of 4096
+// (3.5) 751 and 870, 4 x 4096 (6.9) 539 and 912; 2 x 1024 (3.5) 99 and 127.  Of a
+// packed batch the longest sequence is not known, and cut at the mean it may be
+// little shorter: 5 ragged sequences of 2048 channels, 16384 tokens in all (4.3
+// warps), 592 to 759 us at the mean, 455 to 501 in units for sixteen warps an SM; 3
+// of 4096 (5.2) 964 to 1011 and 849 to 959.  Units for sixteen warps: 20011 packed
+// tokens of 1100 channels 287 us, 348 for twelve.  The two launches more are worth
+// some hundred tokens.
+constexpr int kFewWarps = 3, kFewWarpsPacked = 6, kWantWarps = 16, kShortest = 32, kLeast = 128;
 
 Cut fwd_cut(int B, int T, int D, int S, int N, int packed)
 {
-    return cut_of(B, T, N, packed, (double)D * lanes_of(S) / 64.0, kFewWarps, kWantWarps, kShortest, kLeast);
+    return cut_of(B, T, N, packed, (double)D * lanes_of(S) / 64.0, packed ? kFewWarpsPacked : kFewWarps, kWantWarps,
+                  kShortest, kLeast);
 }
 
 template <typename T, int L>

@@ -41,3 +41,16 @@ def test_workspace_queries_beyond_an_int():
         assert kda.group_norm_workspace_bytes(1, T, 64, 4, 1, False, backward=True) == 0
     assert kda.ssm_scan_fwd_workspace_bytes(1, 4096, 64, 16, 1, 1, False) > 0
     assert kda.group_norm_workspace_bytes(1, 4096, 64, 4, 1, False, backward=True) > 0
+
+
+def test_which_scans_are_cut():
+    """Sequences of one length stay whole from three warps an SM on (of 148: 7104
+    channels of 16 states in all sequences together), ragged ones' limit is six."""
+    def cut(n, T, D, packed, S=16):
+        return kda.ssm_scan_fwd_workspace_bytes(1 if packed else n, n * T if packed else T, D, S, 1, n, packed) > 0
+
+    assert cut(1, 16384, 4096, False) and not cut(2, 8192, 4096, False) and not cut(4, 4096, 4096, False)
+    assert cut(6, 2000, 1024, False) and not cut(7, 2000, 1024, False)
+    assert cut(1, 2000, 1024, False, 64) and not cut(2, 2000, 1024, False, 64)
+    assert not cut(1, 127, 64, False) and cut(1, 128, 64, False)
+    assert cut(2, 8192, 4096, True) and cut(4, 4096, 4096, True)
