@@ -420,7 +420,7 @@ kda_short_conv_params_kernel(const float* __restrict__ part, float* __restrict__
 }
 
 struct Shape {
-    int V, tx, ty, ncb, run;
+    int tx, ty, ncb, run;
     long long tiles, edges;
 };
 
@@ -429,7 +429,6 @@ struct Shape {
 Shape shape_of(int C, int V, int threads, int width)
 {
     Shape s = {};
-    s.V = V;
     const int cols = (C + V - 1) / V;
     s.tx = 1;
     while (s.tx < cols && s.tx < width) s.tx <<= 1;

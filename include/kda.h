@@ -473,7 +473,8 @@ kda_status kda_ssm_step(const void* u, const void* delta, const float* A, const 
  * grad_B, grad_C [B, T, G, S], grad_z [B, T, D] (read and written only where z
  * is given), and, each unless NULL, grad_skip, grad_delta_bias [D] and
  * grad_initial_state [N, D, S].  workspace: kda_ssm_scan_bwd_workspace_bytes()
- * (the state every 8 or 16 tokens and the sums over channels and tokens),
+ * (the state every 4, 8 or 16 tokens, for S up to 4, up to 8 and above, and the
+ * sums over channels and tokens),
  * rules as for kda_chunk_bwd.
  */
 kda_status kda_ssm_scan_bwd(const void* u, const void* delta, const float* A, const void* Bm,
