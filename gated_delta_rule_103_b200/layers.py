@@ -69,11 +69,12 @@ def _activation(name) -> int:
 
 
 def _rank(t: torch.Tensor, name: str, n: int):
-    if t.dim() != n:
-        raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
     shape = t.shape
-    if max(shape) > _INT_MAX:      # ctypes would take it modulo 2^32
-        raise ValueError(f"{name} must have sizes below 2^31, got {tuple(shape)}")
+    if len(shape) != n:
+        raise ValueError(f"{name} must have {n} dimensions, got {len(shape)}")
+    for size in shape:
+        if size > _INT_MAX:       # ctypes would take it modulo 2^32
+            raise ValueError(f"{name} must have sizes below 2^31, got {tuple(shape)}")
     return shape
 
 
