@@ -76,16 +76,16 @@ __device__ __forceinline__ float rate(float A)
 
 // The decay e^(dt A) of one token from A log2 e.  A state carries the mean error
 // of its decays times the tokens it remembers, 1 / |x| with x = dt A.  The fast
-// 2^x is low in the mean by 5e-9 to 7e-9 of its value for x within 2^-9 of zero,
-// by 1.2e-8 to 2.9e-8 from there to -1 (per octave of x, a million values each);
-// a constant in the exponent takes the middle of that back, at no instruction:
-// the product becomes a fused one.  Final states that remember 64, 256, 1024 and
-// 4096 tokens are off by 3e-7, 1.0e-6, 0.9e-6 and 2.3e-6 (without a constant by
-// 1.2e-6, 4.4e-6, 4.2e-6 and 1.5e-5; with 1.8e-8 for every x by 4e-7, 1.5e-6,
-// 8.6e-6 and 3.5e-5).  Which of the two applies is settled for a tile and four
-// states at a time, by the tile's first token and the slowest state (0 where
-// states are padding): 1 to 2 % of the scan's time, where one choice a decay
-// would add half as many instructions as the recurrence has.
+// 2^x is low in the mean by 5e-9 to 7e-9 of its value for x from -2^-14 to -2^-9
+// (1e-8 at -2^-18), by 1.1e-8 to 3.0e-8 from there to -1 (a million values an octave
+// of x, read off the states after one token without input); a constant in the
+// exponent takes the middle of that back, at no instruction: the product becomes a
+// fused one.  Final states that remember 64, 256, 1024 and 4096 tokens are off by
+// 3e-7, 1.0e-6, 0.9e-6 and 2.3e-6 (without a constant by 1.2e-6, 4.4e-6, 4.2e-6 and
+// 1.5e-5; with 1.8e-8 for every x by 4e-7, 1.5e-6, 8.6e-6 and 3.5e-5).  Which of the
+// two applies is settled for a tile and four states at a time, by the tile's first
+// token and the slowest state (0 where states are padding): 1 to 2 % of the scan's
+// time; one choice a decay cost the step 7 %.
 constexpr float kMeanLong = 6e-9f * kLog2e, kMean = 2.2e-8f * kLog2e;
 constexpr float kLongRate = -0.0027f * kLog2e;  // 2^-8.5
 __device__ __forceinline__ float slowest(const float (&A)[4])

@@ -23,7 +23,7 @@ using namespace ssm;
 // computed one token ahead, and the register bound is wide (11 warps an SM; with
 // the compiler's own 128 registers the same code took 712 us against 538).
 //
-// 4 x 4096 tokens of 4096 channels, 16 states, bf16: 529 us.  Its 67 M x 20
+// 4 x 4096 tokens of 4096 channels, 16 states, bf16: 539 us.  Its 67 M x 20
 // special function results take 295 us, its bytes 83 us.  The unit is busy 54 %
 // of the time, issue slots 54 %: two warps a scheduler do not fill more.  Four
 // states of one channel a lane (600 us) and sixteen (977 us) were slower: there
