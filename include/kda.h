@@ -437,7 +437,8 @@ size_t kda_short_conv_bwd_workspace_bytes(int B, int T, int C, int W, int N, int
  *
  *   u, delta, out  [B, T, D]     dtype
  *   A              [D, S]        fp32 (negative for a decaying state; -inf for
- *                                one that each token replaces)
+ *                                one that each token replaces; a growing one's
+ *                                exp(A sum dt) over any tokens has to be finite)
  *   Bm, Cm         [B, T, G, S]  dtype; G divides D, S up to 128
  *   skip, delta_bias  [D]        fp32 or NULL (zero)
  *   z              [B, T, D]     dtype or NULL
